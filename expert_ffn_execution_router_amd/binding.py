@@ -26,6 +26,7 @@ MOE_I_SINGLE_BUFFER = 2
 MOE_W_BF16, MOE_W_FP8_E4M3_B128, MOE_W_MXFP4, MOE_W_NVFP4 = 0, 1, 2, 3
 MOE_ACT_DEFAULT, MOE_ACT_MXFP6 = 0, 1
 MOE_QUANT_MXFP6 = 64
+MOE_T_BF16, MOE_T_F16, MOE_T_F32 = 0, 1, 2
 MOE_POLICY_OFFLOAD, MOE_POLICY_HOST, MOE_POLICY_HYBRID = 0, 1, 2
 
 
@@ -76,6 +77,7 @@ class moe_profile(ctypes.Structure):
 
 
 _vp, _i, _sz, _d = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_double
+_ll = ctypes.c_longlong
 _P = ctypes.POINTER
 
 # name -> (restype, argtypes), in the order of include/moe.h
@@ -112,6 +114,15 @@ SIGNATURES = {
     "moe_check_device_error": (_i, [_vp]),
     "moe_profile_begin": (_i, [_vp, _i, ctypes.c_uint]),
     "moe_profile_end": (_i, [_vp, _P(moe_profile)]),
+    "moe_sort_rows": (_ll, [_i, _i, _i, _i]),
+    "moe_sort_workspace_bytes": (_sz, [_i, _i, _i]),
+    "moe_sort": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _vp, _ll, _vp, _vp, _sz, _vp]),
+    "moe_permute": (_i, [_i, _vp, _ll, _vp, _vp, _i, _i, _ll, _i, _vp, _ll, _vp]),
+    "moe_unpermute": (_i, [_i, _vp, _ll, _ll, _vp, _vp, _vp, _ll, _i, _i, _i, _i, _vp, _ll, _vp]),
+    "moe_unpermute_backward": (_i, [_i, _vp, _ll, _i, _vp, _ll, _vp, _ll, _vp, _vp, _i, _i, _i, _vp, _ll, _vp, _vp]),
+    "moe_gate_backward": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _ll, _vp]),
+    "moe_w4_matmul": (_i, [_i, _vp, _ll, _ll, _vp, _i, _vp, _vp, _i, _ll, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _vp,
+                           _ll, _vp]),
 }
 
 _lib = None
@@ -188,6 +199,14 @@ prefill_stream_layer = _fn("prefill_stream_layer")
 moe_check_device_error = _fn("moe_check_device_error")
 moe_profile_begin = _fn("moe_profile_begin")
 moe_profile_end = _fn("moe_profile_end")
+moe_sort_rows = _fn("moe_sort_rows")
+moe_sort_workspace_bytes = _fn("moe_sort_workspace_bytes")
+moe_sort = _fn("moe_sort")
+moe_permute = _fn("moe_permute")
+moe_unpermute = _fn("moe_unpermute")
+moe_unpermute_backward = _fn("moe_unpermute_backward")
+moe_gate_backward = _fn("moe_gate_backward")
+moe_w4_matmul = _fn("moe_w4_matmul")
 
 
 def make_config(L, E, k, H, I, wfmt, n_slots, max_tokens, host_threads=0) -> moe_config:

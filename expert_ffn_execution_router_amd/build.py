@@ -16,7 +16,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 
 HIP_SOURCES = ["route.hip", "gemm_dec.hip", "gemm_pf.hip", "gemv.hip", "gemm_pf8.hip", "combine.hip", "slots.hip",
-               "noalloc.hip"]
+               "noalloc.hip", "dispatch.hip", "w4.hip"]
 # Per-source code-generation options (none at present).
 HIP_EXTRA = {}
 HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",

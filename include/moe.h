@@ -79,6 +79,8 @@ enum { MOE_W_BF16 = 0, MOE_W_FP8_E4M3_B128 = 1, MOE_W_MXFP4 = 2, MOE_W_NVFP4 = 3
 enum { MOE_ACT_DEFAULT = 0, MOE_ACT_MXFP6 = 1 };   /* moe_set_activations */
 enum { MOE_QUANT_MXFP6 = 64 };                      /* moe_quantize format code */
 
+enum { MOE_T_BF16 = 0, MOE_T_F16 = 1, MOE_T_F32 = 2 };  /* element types of the operators below */
+
 /* Miss policy (paper.oopus.info review, section 5 lists the backend switch
  * offload / cpu / hybrid): OFFLOAD fills every miss (q = m), HOST executes
  * every miss on the host (q = 0), HYBRID uses q* = round(m B_P / B_H),
@@ -455,6 +457,94 @@ typedef struct {
 int moe_profile_begin(moe_ctx* ctx, int max_launches, unsigned stage_mask);
 /* Synchronises the device, sums the records into out and stops timing. */
 int moe_profile_end(moe_ctx* ctx, moe_profile* out);
+
+/* ------------------------------------------------------------------------
+ * Operators of their own: expert dispatch with its gradients, and products
+ * with 4-bit weights.  No context; every pointer is device memory; sizes,
+ * types and strides are checked on the host before any device work (message
+ * in moe_last_error(NULL)).  Rows have a stride (ld*, in elements, at least
+ * the width) and contiguous values.  Calls only enqueue kernels on stream, so
+ * they can be captured, and they keep nothing between calls: calls on
+ * different streams are independent as long as their outputs and workspaces
+ * are.  Equal inputs give equal bits.  T = 0 and rows = 0 are valid.
+ * ------------------------------------------------------------------------ */
+
+/* (token, choice) pairs sorted by expert.  Pair a = t*k + j of ids (int32
+ * [T, k]) is kept if 0 <= ids[a] < E, else dropped (a padded token, an expert
+ * of another rank).
+ *   counts  int32 [E]     kept pairs per expert
+ *   offsets int32 [E+1]   first grouped row of each expert; segments are
+ *                         counts rounded up to a multiple of align (1: packed)
+ *   perm    int32 [rows]  pair of a grouped row; -1 in a segment's padding;
+ *                         -2 in the rows behind offsets[E]
+ *   pos     int32 [T, k]  grouped row of a pair, -1 if dropped
+ * Pairs of one expert keep their order.  rows: the length of perm, at least
+ * moe_sort_rows (T*k + min(E, T*k)*(align-1), every routing fits).  ws:
+ * moe_sort_workspace_bytes bytes (0 for at most 2048 pairs: ws may be NULL).
+ * E <= 1024, k <= 64, T*k < 2^31.  INVAL, UNSUPPORTED, HIP. */
+int64_t moe_sort_rows(int T, int k, int E, int align);
+size_t moe_sort_workspace_bytes(int T, int k, int E);
+int moe_sort(const int32_t* ids, int T, int k, int E, int align, int32_t* counts, int32_t* offsets, int32_t* perm,
+             int64_t rows, int32_t* pos, void* ws, size_t ws_bytes, void* stream);
+
+/* Token rows to their grouped places: out[pos[t,j]] = x[t], for each pair
+ * with 0 <= pos < rows.  x [T, cols], out [rows, cols] of one MOE_T_* type.
+ * perm (may be NULL: no padding): rows with perm = -1 are set to zero; rows
+ * behind the last segment are left as they were.  The gradient of this call
+ * is moe_unpermute without weights. */
+int moe_permute(int dtype, const void* x, int64_t ldx, const int32_t* perm, const int32_t* pos, int T, int k,
+                int64_t rows, int cols, void* out, int64_t ldo, void* stream);
+
+/* Grouped rows back to tokens: out[t] = base[t] + sum_j w[t,j] y[pos[t,j]]
+ * over the pairs with 0 <= pos < rows, fp32 sums in choice order on top of
+ * base, rounded once.  y [rows, cols]; w fp32 [T, k], or NULL for ones; base
+ * fp32 [T, cols] or NULL for zero (a host partial, a shared expert's output;
+ * it may be out itself when out is fp32).  A token whose pairs are all
+ * dropped gets base.  Types: equal, or one of y and out fp32. */
+int moe_unpermute(int ytype, const void* y, int64_t ldy, int64_t rows, const int32_t* pos, const float* w,
+                  const float* base, int64_t ldb, int T, int k, int cols, int otype, void* out, int64_t ldo,
+                  void* stream);
+
+/* Gradients of moe_unpermute: dy[pos[t,j]] = w[t,j] dout[t] (type of y,
+ * rounded once) and dw[t,j] = <dout[t], y[pos[t,j]]> (fp32 [T, k]; 0 for a
+ * dropped pair), the gradient of base being dout.  perm as in moe_permute:
+ * dy's padding rows are set to zero, rows behind the last segment left as
+ * they were.  dout has out's type (otype), dy y's; dy must not be y. */
+int moe_unpermute_backward(int otype, const void* dout, int64_t ldd, int ytype, const void* y, int64_t ldy,
+                           const int32_t* perm, int64_t rows, const int32_t* pos, const float* w, int T, int k,
+                           int cols, void* dy, int64_t lddy, float* dw, void* stream);
+
+/* Gradient of the gate: w = softmax over the k chosen logits (moe_route), so
+ * dz[t,e] = sum over j with ids[t,j] = e of w_j (dw_j - sum_i w_i dw_i), and
+ * 0 for experts that were not chosen.  ids int32, w and dw fp32 [T, k]; dz
+ * fp32 [T, E] with row stride ldz, written whole.  ids outside [0, E) take
+ * part in the inner sum only. */
+int moe_gate_backward(const int32_t* ids, const float* w, const float* dw, int T, int k, int E, float* dz, int64_t ldz,
+                      void* stream);
+
+/* Few rows times 4-bit weights with group scales:
+ *   z[r,n] = sum_k x[r,k] (q[n,k] - zero[n,k/group]) scale[n,k/group]
+ * codes uint8 [E][N][K/2], two per byte, even input in the low nibble, on 16
+ * bytes; scales [E][N][K/group] (bf16 or fp16, stype); zeros the same shape
+ * in x's type, or NULL for 8.  group 32, 64 or a multiple of 128 that divides
+ * K.  Products are exact, sums fp32, out (x's type or fp32) rounded once.
+ * gated != 0: the matrix is [gate; up] stacked (N even) and
+ * out[r] = silu(z[r, :N/2]) * z[r, N/2:], [rows, N/2]; else out [rows, N].
+ * x bf16 or fp16 [x_rows, K], on 16 bytes, stride a multiple of 8, finite (a
+ * row with an infinity or NaN gives NaN, other rows are not touched by it).
+ *   dense (offsets NULL, E = 1): out row r from x row r.
+ *   per expert: grouped rows offsets[e] .. + counts[e] (counts NULL: up to
+ *     offsets[e+1]) use matrix e; offsets int32 [E+1], counts int32 [E] as
+ *     moe_sort gives them.  Rows in no segment are left as they were.
+ *   row_map (int32 [rows] or NULL): grouped row r reads x row
+ *     row_map[r] / map_div (moe_sort's perm with map_div = k reads token
+ *     rows); a map entry outside x reads a row of zeros.
+ * Any number of rows is valid; the design point is up to 64 per matrix.
+ * E <= 1024.  INVAL, UNSUPPORTED (dense: over 1048560 rows), HIP. */
+int moe_w4_matmul(int xtype, const void* x, int64_t ldx, int64_t x_rows, const int32_t* row_map, int map_div,
+                  const int32_t* offsets, const int32_t* counts, int E, int64_t rows, const uint8_t* codes, int stype,
+                  const void* scales, const void* zeros, int N, int K, int group, int gated, int otype, void* out,
+                  int64_t ldo, void* stream);
 
 #ifdef __cplusplus
 }

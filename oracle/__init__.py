@@ -7,6 +7,8 @@ HIP library (expert_ffn_execution_router_amd) and never imports it.
   formats  exact decoding of bf16 / OCP E4M3FN / OCP MX (E2M1, E8M0)
   moe      routing, grouping, SwiGLU experts, the layer (exact and mirrored)
   cache    global LRU slot model, q* split, link-bound prefill time
+  dispatch pairs sorted by expert, rows there and back, and the gradients
+  w4       products with 4-bit weights and group scales
 
 Every function is pinned by tests/test_oracle_*.py against values that do not
 come from the oracle itself (format definitions, hand-computed worked
