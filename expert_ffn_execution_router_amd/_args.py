@@ -1,5 +1,8 @@
 """Checks and launch plumbing shared by the operator modules (dispatch, w4):
-a wrong type, shape, stride or device is an error here, before any kernel."""
+a wrong type, shape, stride or device is an error here, before any kernel.
+
+A single-token call's kernels take a few microseconds, so the checks read
+each tensor property once and compare plain integers."""
 from __future__ import annotations
 
 import torch
@@ -7,58 +10,66 @@ import torch
 from . import binding as B
 
 TYPES = {torch.bfloat16: B.MOE_T_BF16, torch.float16: B.MOE_T_F16, torch.float32: B.MOE_T_F32}
+F32_ONLY = {torch.float32: B.MOE_T_F32}
+BYTES = {B.MOE_T_BF16: 2, B.MOE_T_F16: 2, B.MOE_T_F32: 4}
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def rows(name, t, device, cols=None, types=TYPES):
-    """A [n, cols] tensor with contiguous rows: (type code, row stride)."""
-    if t.dtype not in types:
+def rows(name, t, dev, n, cols, types=TYPES):
+    """A tensor of n rows (any number if None) of cols contiguous values on
+    device index dev: (type code, address, row stride, address of its end)."""
+    code = types.get(t.dtype)
+    if code is None:
         raise ValueError(f"{name}: type {t.dtype} is not one of {[str(x) for x in types]}")
-    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [rows{'' if cols is None else f', {cols}'}]")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    n, c = t.shape
-    step = t.stride(0) if n > 1 else c
-    if n and ((c > 1 and t.stride(1) != 1) or step < c):
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols or (n is not None and shape[0] != n):
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [{'rows' if n is None else n}, {cols}]")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected device {dev}")
+    p, m = t.data_ptr(), shape[0]
+    if m == 0:
+        return code, p, cols, p
+    step, one = t.stride()
+    if m == 1:
+        step = cols
+    if (one != 1 and cols > 1) or step < cols:
         raise ValueError(f"{name}: rows have to be contiguous and must not overlap (strides {tuple(t.stride())})")
-    return types[t.dtype], step
+    return code, p, step, p + ((m - 1) * step + cols) * BYTES[code]
 
 
-def whole(name, t, device, dtype, shape):
-    """A contiguous tensor of one type and shape."""
+def whole(name, t, dev, dtype, shape):
+    """Address of a contiguous tensor of one type and shape."""
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected {dtype} {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected device {dev}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: has to be contiguous")
     return t.data_ptr()
 
 
-def apart(name, out, *others):
-    """out must not share memory with what the kernels read while writing it."""
-    a0 = out.data_ptr()
-    a1 = a0 + _span(out)
-    for t in others:
-        if t is not None and t.data_ptr() < a1 and a0 < t.data_ptr() + _span(t):
-            raise ValueError(f"{name}: overlaps an input")
+def apart(name, p, end, q, qend):
+    """The written range [p, end) must not meet the read range [q, qend)."""
+    if q < end and p < qend:
+        raise ValueError(f"{name}: overlaps an input")
 
 
-def _span(t):
-    if t.numel() == 0:
-        return 0
-    return (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
-
-
-def launch(fn, device, stream, *args):
-    """fn(*args, stream) with device current; stream: a torch stream of that
-    device, or None for its current one."""
-    if device.type != "cuda":
-        raise ValueError(f"tensors have to be on the GPU, got {device}")
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream of {stream.device}, tensors on {device}")
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    if device.index == torch.cuda.current_device():
-        return B.check(fn(*args, s.cuda_stream))
-    with torch.cuda.device(device):
-        return B.check(fn(*args, s.cuda_stream))
+def launch(fn, dev, stream, *args):
+    """fn(*args, stream) with the tensors' device current; stream: a torch
+    stream of that device, or None for its current one."""
+    if dev < 0:
+        raise ValueError("tensors have to be on the GPU")
+    if stream is None:
+        s = _raw_stream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"stream of {stream.device}, tensors on device {dev}")
+    else:
+        s = stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, s)
+    if rc < 0:
+        B.check(rc)

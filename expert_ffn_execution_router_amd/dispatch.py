@@ -24,6 +24,9 @@ import torch
 from . import _args as A
 from . import binding as B
 
+_I32, _F32 = torch.int32, torch.float32
+_lib = B.lib
+
 
 def sort_rows(T: int, k: int, E: int, align: int = 1) -> int:
     """Rows perm (and the grouped tensors) need for any routing of T tokens."""
@@ -41,72 +44,64 @@ def sort(ids, counts, offsets, perm, pos, align=1, ws=None, stream=None):
     """Groups the pairs of ids by expert, segments padded to multiples of
     align.  ws: uint8 tensor of sort_workspace_bytes; None allocates one where
     it is needed (more than 2048 pairs)."""
-    if ids.dim() != 2:
-        raise ValueError(f"ids: shape {tuple(ids.shape)}, expected [T, k]")
-    T, k = ids.shape
-    dev, E = ids.device, counts.numel()
-    i32 = torch.int32
-    need = B.moe_sort_workspace_bytes(T, k, E)
-    if need and ws is None:
-        if stream is None:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        else:
-            with torch.cuda.stream(stream):
-                ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    shape = ids.shape
+    if len(shape) != 2:
+        raise ValueError(f"ids: shape {tuple(shape)}, expected [T, k]")
+    T, k = shape
+    dev, E, rows = ids.get_device(), counts.numel(), perm.numel()
+    args = (A.whole("ids", ids, dev, _I32, shape), T, k, E, align, A.whole("counts", counts, dev, _I32, (E,)),
+            A.whole("offsets", offsets, dev, _I32, (E + 1,)), A.whole("perm", perm, dev, _I32, (rows,)), rows,
+            A.whole("pos", pos, dev, _I32, shape))
+    if ws is None:
+        need = B.moe_sort_workspace_bytes(T, k, E) if T * k > 2048 else 0
+        if need and dev >= 0:
+            if stream is None:
+                ws = torch.empty(need, dtype=torch.uint8, device=ids.device)
+            else:
+                with torch.cuda.stream(stream):
+                    ws = torch.empty(need, dtype=torch.uint8, device=ids.device)
     wp, wn = (None, 0) if ws is None else (A.whole("ws", ws, dev, torch.uint8, (ws.numel(),)), ws.numel())
-    rows = perm.numel()
-    A.launch(B.moe_sort, dev, stream, A.whole("ids", ids, dev, i32, (T, k)), T, k, E, align,
-             A.whole("counts", counts, dev, i32, (E,)), A.whole("offsets", offsets, dev, i32, (E + 1,)),
-             A.whole("perm", perm, dev, i32, (rows,)), rows, A.whole("pos", pos, dev, i32, (T, k)), wp, wn)
+    A.launch(_lib().moe_sort, dev, stream, *args, wp, wn)
 
 
-def _pos(pos, dev):
-    if pos.dim() != 2:
-        raise ValueError(f"pos: shape {tuple(pos.shape)}, expected [T, k]")
-    T, k = pos.shape
-    return A.whole("pos", pos, dev, torch.int32, (T, k)), T, k
+def _tokens(name, pos, dev):
+    shape = pos.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [T, k]")
+    return A.whole(name, pos, dev, _I32, shape), shape
 
 
 def permute(x, perm, pos, out, stream=None):
     """out[pos[t, j]] = x[t]; rows with perm -1 become zero, rows behind the
     last segment stay.  perm None: no padding rows (align 1)."""
-    dev = x.device
-    pp, T, k = _pos(pos, dev)
-    dt, ldx = A.rows("x", x, dev)
-    if x.shape[0] != T:
-        raise ValueError(f"x: {x.shape[0]} rows, pos has {T} tokens")
-    if out.dtype != x.dtype:
+    dev, cols, n = x.get_device(), x.shape[-1], out.shape[0]
+    pp, (T, k) = _tokens("pos", pos, dev)
+    dt, xp, ldx, xe = A.rows("x", x, dev, T, cols)
+    ot, op, ldo, oe = A.rows("out", out, dev, n, cols)
+    if ot != dt:
         raise ValueError(f"out: type {out.dtype}, x has {x.dtype}")
-    _, ldo = A.rows("out", out, dev, x.shape[1])
-    A.apart("out", out, x)
-    rows = out.shape[0]
-    rp = None if perm is None else A.whole("perm", perm, dev, torch.int32, (rows,))
-    A.launch(B.moe_permute, dev, stream, dt, x.data_ptr(), ldx, rp, pp, T, k, rows, x.shape[1], out.data_ptr(), ldo)
+    A.apart("out", op, oe, xp, xe)
+    rp = None if perm is None else A.whole("perm", perm, dev, _I32, (n,))
+    A.launch(_lib().moe_permute, dev, stream, dt, xp, ldx, rp, pp, T, k, n, cols, op, ldo)
 
 
 def unpermute(y, pos, w, out, base=None, stream=None):
     """out[t] = base[t] + sum_j w[t, j] y[pos[t, j]] over the kept pairs, summed
     in fp32.  w: fp32 [T, k] or None for ones; base: fp32 [T, cols] or None.
     y and out: one type, or one of them fp32."""
-    dev = y.device
-    pp, T, k = _pos(pos, dev)
-    yt, ldy = A.rows("y", y, dev)
-    cols = y.shape[1]
-    ot, ldo = A.rows("out", out, dev, cols)
-    if out.shape[0] != T:
-        raise ValueError(f"out: {out.shape[0]} rows, pos has {T} tokens")
-    A.apart("out", out, y)
-    wp = None if w is None else A.whole("w", w, dev, torch.float32, (T, k))
+    dev, cols, n = y.get_device(), y.shape[-1], y.shape[0]
+    pp, shape = _tokens("pos", pos, dev)
+    T, k = shape
+    yt, yp, ldy, ye = A.rows("y", y, dev, n, cols)
+    ot, op, ldo, oe = A.rows("out", out, dev, T, cols)
+    A.apart("out", op, oe, yp, ye)
+    wp = None if w is None else A.whole("w", w, dev, _F32, shape)
     bp, ldb = None, 0
     if base is not None:
-        _, ldb = A.rows("base", base, dev, cols, {torch.float32: B.MOE_T_F32})
-        if base.shape[0] != T:
-            raise ValueError(f"base: {base.shape[0]} rows, pos has {T} tokens")
-        bp = base.data_ptr()
-        if bp != out.data_ptr() or ldb != ldo or out.dtype != torch.float32:
-            A.apart("out", out, base)
-    A.launch(B.moe_unpermute, dev, stream, yt, y.data_ptr(), ldy, y.shape[0], pp, wp, bp, ldb, T, k, cols, ot,
-             out.data_ptr(), ldo)
+        _, bp, ldb, be = A.rows("base", base, dev, T, cols, A.F32_ONLY)
+        if bp != op or ldb != ldo or ot != B.MOE_T_F32:       # else in place
+            A.apart("out", op, oe, bp, be)
+    A.launch(_lib().moe_unpermute, dev, stream, yt, yp, ldy, n, pp, wp, bp, ldb, T, k, cols, ot, op, ldo)
 
 
 def permute_backward(dout, pos, dx, stream=None):
@@ -118,34 +113,29 @@ def unpermute_backward(dout, y, perm, pos, w, dy, dw, stream=None):
     """Gradients of unpermute: dy[pos[t, j]] = w[t, j] dout[t] and dw[t, j] =
     <dout[t], y[pos[t, j]]> (0 for dropped pairs).  Padding rows of dy become
     zero (perm None: there are none), rows behind the last segment stay."""
-    dev = y.device
-    pp, T, k = _pos(pos, dev)
-    yt, ldy = A.rows("y", y, dev)
-    rows, cols = y.shape
-    ot, ldd = A.rows("dout", dout, dev, cols)
-    if dout.shape[0] != T:
-        raise ValueError(f"dout: {dout.shape[0]} rows, pos has {T} tokens")
-    if dy.dtype != y.dtype or dy.shape != y.shape:
-        raise ValueError(f"dy: {dy.dtype} {tuple(dy.shape)}, y is {y.dtype} {tuple(y.shape)}")
-    _, lddy = A.rows("dy", dy, dev, cols)
-    A.apart("dy", dy, y, dout)
-    rp = None if perm is None else A.whole("perm", perm, dev, torch.int32, (rows,))
-    A.launch(B.moe_unpermute_backward, dev, stream, ot, dout.data_ptr(), ldd, yt, y.data_ptr(), ldy, rp, rows, pp,
-             A.whole("w", w, dev, torch.float32, (T, k)), T, k, cols, dy.data_ptr(), lddy,
-             A.whole("dw", dw, dev, torch.float32, (T, k)))
+    dev, cols, n = y.get_device(), y.shape[-1], y.shape[0]
+    pp, shape = _tokens("pos", pos, dev)
+    T, k = shape
+    yt, yp, ldy, ye = A.rows("y", y, dev, n, cols)
+    ot, gp, ldd, ge = A.rows("dout", dout, dev, T, cols)
+    dt, dp, lddy, de = A.rows("dy", dy, dev, n, cols)
+    if dt != yt:
+        raise ValueError(f"dy: type {dy.dtype}, y has {y.dtype}")
+    A.apart("dy", dp, de, yp, ye)
+    A.apart("dy", dp, de, gp, ge)
+    rp = None if perm is None else A.whole("perm", perm, dev, _I32, (n,))
+    A.launch(_lib().moe_unpermute_backward, dev, stream, ot, gp, ldd, yt, yp, ldy, rp, n, pp,
+             A.whole("w", w, dev, _F32, shape), T, k, cols, dp, lddy, A.whole("dw", dw, dev, _F32, shape))
 
 
 def gate_backward(ids, w, dw, dlogits, stream=None):
     """Gradient of the softmax over the chosen logits: dlogits fp32 [T, E],
     zero where an expert was not chosen."""
-    dev = ids.device
-    if ids.dim() != 2:
-        raise ValueError(f"ids: shape {tuple(ids.shape)}, expected [T, k]")
-    T, k = ids.shape
-    _, ldz = A.rows("dlogits", dlogits, dev, None, {torch.float32: B.MOE_T_F32})
-    if dlogits.shape[0] != T:
-        raise ValueError(f"dlogits: {dlogits.shape[0]} rows, ids has {T} tokens")
-    A.apart("dlogits", dlogits, w, dw)
-    A.launch(B.moe_gate_backward, dev, stream, A.whole("ids", ids, dev, torch.int32, (T, k)),
-             A.whole("w", w, dev, torch.float32, (T, k)), A.whole("dw", dw, dev, torch.float32, (T, k)), T, k,
-             dlogits.shape[1], dlogits.data_ptr(), ldz)
+    dev, E = ids.get_device(), dlogits.shape[-1]
+    ip, shape = _tokens("ids", ids, dev)
+    T, k = shape
+    _, zp, ldz, ze = A.rows("dlogits", dlogits, dev, T, E, A.F32_ONLY)
+    wp, dp = A.whole("w", w, dev, _F32, shape), A.whole("dw", dw, dev, _F32, shape)
+    A.apart("dlogits", zp, ze, wp, wp + 4 * T * k)
+    A.apart("dlogits", zp, ze, dp, dp + 4 * T * k)
+    A.launch(_lib().moe_gate_backward, dev, stream, ip, wp, dp, T, k, E, zp, ldz)

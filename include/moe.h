@@ -540,7 +540,8 @@ int moe_gate_backward(const int32_t* ids, const float* w, const float* dw, int T
  *     row_map[r] / map_div (moe_sort's perm with map_div = k reads token
  *     rows); a map entry outside x reads a row of zeros.
  * Any number of rows is valid; the design point is up to 64 per matrix.
- * E <= 1024.  INVAL, UNSUPPORTED (dense: over 1048560 rows), HIP. */
+ * E <= 1024, K <= 32768, at least 4 groups in all unless group = K.  INVAL,
+ * UNSUPPORTED, HIP. */
 int moe_w4_matmul(int xtype, const void* x, int64_t ldx, int64_t x_rows, const int32_t* row_map, int map_div,
                   const int32_t* offsets, const int32_t* counts, int E, int64_t rows, const uint8_t* codes, int stype,
                   const void* scales, const void* zeros, int N, int K, int group, int gated, int otype, void* out,

@@ -69,7 +69,8 @@ def check(out, x, q, s, z, group, gated):
 
 SIZES = [(1, 2048, 2048, 128), (1, 16, 32, 32), (3, 1, 64, 64), (5, 1003, 2080, 32), (7, 100, 192, 64),
          (16, 50, 768, 128), (17, 33, 768, 256), (31, 130, 1024, 32), (33, 64, 1088, 64), (64, 260, 2048, 128),
-         (65, 20, 512, 512), (150, 34, 96, 32), (0, 8, 64, 32)]
+         (65, 20, 512, 512), (150, 34, 96, 32), (0, 8, 64, 32), (2, 48, 4096, 128), (18, 40, 3968, 64),
+         (17, 34, 6144, 32), (3, 33, 5120, 1024), (4, 20, 8320, 64), (2, 18, 16384, 128)]
 
 
 @pytest.mark.parametrize("xt,st,ot", [(BF, BF, BF), (BF, HF, F32), (HF, HF, HF), (HF, BF, F32)])
@@ -150,7 +151,8 @@ def grouped(T, k, E, seed, skew=False, drop=0.0, align=1, extra=0):
 GROUPED = [(1, 8, 128, 96, 256, 128, False, 0.0, 1), (1, 1, 1, 40, 64, 32, False, 0.0, 1),
            (5, 3, 70, 36, 192, 64, False, 0.2, 1), (64, 8, 32, 64, 256, 128, True, 0.0, 1),
            (64, 4, 130, 34, 160, 32, True, 0.3, 16), (300, 2, 5, 48, 128, 64, True, 0.0, 8),
-           (6, 2, 9, 16, 64, 32, False, 1.0, 4)]
+           (6, 2, 9, 16, 64, 32, False, 1.0, 4), (40, 3, 300, 44, 4096, 64, True, 0.1, 1),
+         (9, 2, 6, 70, 8448, 128, False, 0.0, 1)]
 
 
 @pytest.mark.parametrize("xt,ot,zeros", [(BF, BF, False), (HF, F32, True), (BF, F32, True)])

@@ -94,7 +94,8 @@ def test_w4_refusals(B):
                 dict(ldo=31), dict(gated=1, ldo=15), dict(x=None), dict(codes=None), dict(scales=None),
                 dict(out=None), dict(x=P + 8), dict(codes=P + 8)):
         assert mm(**bad) == B.MOE_E_INVAL, bad
-    assert mm(rows=1048561, xr=1048561) == B.MOE_E_UNSUPPORTED
+    assert mm(K=32896, ldx=32896) == B.MOE_E_UNSUPPORTED
+    assert mm(N=1, K=64, group=32, ldx=64) == B.MOE_E_UNSUPPORTED          # fewer than 4 groups in all
     assert mm(rows=0) == 0
 
 
