@@ -11,9 +11,9 @@
 //
 // Every sum is fp32 in a fixed order and every rank is counted, not drawn
 // from an atomic, so equal inputs give equal bits.
-#include "common.h"
 #include "fwd_ws.h"
 #include "moe.h"
+#include "route_dev.h"
 
 namespace {
 
@@ -29,16 +29,6 @@ namespace {
 constexpr int SORT_WAVES = 8, SORT_THREADS = SORT_WAVES * 64, SORT_ROUNDS = 4;
 constexpr int SORT_SPAN = SORT_THREADS * SORT_ROUNDS;      // pairs per block of a multi-block sort
 constexpr int SORT_MAX_E = 1024;
-
-DEV int wave_incl(int v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int u = __shfl_up(v, off, 64);
-    if (lane >= off) v += u;
-  }
-  return v;
-}
 
 // Ranks of the block's pairs inside their wave's run; cnt (LDS, zeroed
 // here): [SORT_WAVES][E] pairs of each expert in each wave's run.
@@ -84,7 +74,7 @@ DEV void rank_pairs(const int32_t* __restrict__ ids, long p0, long n, int E, int
 DEV int scan_experts(int c0, int c1, int align, int* tmp, int& o0, int& o1) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int a0 = (c0 + align - 1) / align * align, a1 = (c1 + align - 1) / align * align;
-  const int inc = wave_incl(a0 + a1);
+  const int inc = wave_incl_sum(a0 + a1);
   if (lane == 63) tmp[wave] = inc;
   __syncthreads();
   int base = 0, end = 0;
@@ -210,49 +200,28 @@ sort_scan_kernel(int32_t* __restrict__ hist, int nblk, int E) {
 // ---------------------------------------------------------------------------
 // rows
 // ---------------------------------------------------------------------------
-// A row is moved by `tpr` threads (a power of two up to 256, at least the
-// row's units where it has fewer), 256 / tpr rows to a workgroup.
+// A row is moved in units of V values (16 bytes of the narrower type), the
+// last one starting early where the width does not divide, so that it writes
+// some values again, with what they hold; rows narrower than a unit go value
+// by value.  Units need no alignment beyond the value's.  tpr threads (a
+// power of two up to 256) move a row, 256 / tpr rows to a workgroup; at 256 a
+// row's index is the workgroup's, so its places and weights are read by scalar
+// loads.
 struct RowMap {
   int tpr_log2;
 };
 
+template <bool WHOLE>
 DEV int row_of(const RowMap m, long& row) {
+  if (WHOLE) {
+    row = blockIdx.x;
+    return threadIdx.x;
+  }
   row = ((long)blockIdx.x << (8 - m.tpr_log2)) + (threadIdx.x >> m.tpr_log2);
   return threadIdx.x & ((1 << m.tpr_log2) - 1);
 }
 
 constexpr int PAD_ROWS = 16;      // grouped rows a padding workgroup looks over
-
-// Copy of token rows to their grouped places, in units U of 16, 4 or 2
-// bytes: each token row is read once and stored k times.  Workgroups past
-// the tokens zero the padding rows (perm -1).
-template <typename U>
-__global__ void __launch_bounds__(256)
-permute_kernel(const U* __restrict__ x, long ldx, const int32_t* __restrict__ pos, long T, int k,
-               const int32_t* __restrict__ perm, long rows, int units, unsigned tok_blocks, RowMap m,
-               U* __restrict__ out, long ldo) {
-  if (blockIdx.x >= tok_blocks) {
-    const long r0 = (long)(blockIdx.x - tok_blocks) * PAD_ROWS;
-    for (int i = 0; i < PAD_ROWS; ++i) {
-      const long r = r0 + i;
-      if (r >= rows) return;
-      if (perm[r] != -1) continue;
-      for (int u = threadIdx.x; u < units; u += 256) out[r * ldo + u] = U{};
-    }
-    return;
-  }
-  long t;
-  const int u0 = row_of(m, t);
-  if (t >= T) return;
-  const int32_t* ps = pos + t * k;
-  for (int u = u0; u < units; u += 1 << m.tpr_log2) {
-    const U v = x[t * ldx + u];
-    for (int j = 0; j < k; ++j) {
-      const int p = ps[j];
-      if ((uint32_t)p < (uint64_t)rows) out[(long)p * ldo + u] = v;
-    }
-  }
-}
 
 template <int DT>
 struct Elem;
@@ -275,80 +244,151 @@ struct Elem<MOE_T_F32> {
   static DEV float store(float v) { return v; }
 };
 
-// V values at p: one 16-byte access for V * size = 16, two for 32, single
-// values for V = 1.
+// V values, aligned as one is.
+template <typename T, int V>
+struct Pack {
+  T v[V];
+};
+
 template <int DT, int V>
 DEV void load_vals(const typename Elem<DT>::type* p, float (&f)[V]) {
-  typedef typename Elem<DT>::type T;
-  struct alignas(V * sizeof(T) >= 16 ? 16 : sizeof(T)) Pack { T v[V]; };
-  const Pack a = *(const Pack*)p;
+  Pack<typename Elem<DT>::type, V> a;
+  __builtin_memcpy(&a, p, sizeof(a));
 #pragma unroll
   for (int i = 0; i < V; ++i) f[i] = Elem<DT>::load(a.v[i]);
 }
 
 template <int DT, int V>
 DEV void store_vals(typename Elem<DT>::type* p, const float (&f)[V]) {
-  typedef typename Elem<DT>::type T;
-  struct alignas(V * sizeof(T) >= 16 ? 16 : sizeof(T)) Pack { T v[V]; };
-  Pack a;
+  Pack<typename Elem<DT>::type, V> a;
 #pragma unroll
   for (int i = 0; i < V; ++i) a.v[i] = Elem<DT>::store(f[i]);
-  *(Pack*)p = a;
+  __builtin_memcpy(p, &a, sizeof(a));
 }
 
-constexpr int JB = 8;             // choices whose rows are in flight together
+// The value is in registers here (else each store's branch loads it again).
+template <typename T, int V>
+DEV void pin(Pack<T, V>& v) {
+  if constexpr (sizeof(v) == 16) {
+    i32x4_t r;
+    __builtin_memcpy(&r, &v, sizeof(v));
+    asm volatile("" : "+v"(r));
+    __builtin_memcpy(&v, &r, sizeof(v));
+  } else {
+    asm volatile("" : "+v"(v.v[0]));
+  }
+}
+
+// Copy of token rows to their grouped places: each token row is read once and
+// stored k times.  Workgroups past the tokens zero the padding rows (perm -1).
+template <typename T, int V, bool WHOLE>
+__global__ void __launch_bounds__(256)
+permute_kernel(const T* __restrict__ x, long ldx, const int32_t* __restrict__ pos, long nT, int k,
+               const int32_t* __restrict__ perm, long rows, int cols, unsigned tok_blocks, RowMap m,
+               T* __restrict__ out, long ldo) {
+  if (blockIdx.x >= tok_blocks) {
+    const Pack<T, V> zero = {};
+    const long r0 = (long)(blockIdx.x - tok_blocks) * PAD_ROWS;
+    for (int i = 0; i < PAD_ROWS; ++i) {
+      const long r = r0 + i;
+      if (r >= rows) return;
+      if (perm[r] != -1) continue;
+      for (int c = threadIdx.x * V; c < cols; c += 256 * V)
+        __builtin_memcpy(out + r * ldo + min(c, cols - V), &zero, sizeof(zero));
+    }
+    return;
+  }
+  long t;
+  const int u0 = row_of<WHOLE>(m, t);
+  if (t >= nT) return;
+  for (int j0 = 0; j0 < k; j0 += 8) {
+    int p[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] = j0 + j < k ? pos[t * k + j0 + j] : -1;
+    for (int c = u0 * V; c < cols; c += V << m.tpr_log2) {
+      const int at = min(c, cols - V);
+      Pack<T, V> v;
+      __builtin_memcpy(&v, x + t * ldx + at, sizeof(v));
+      pin(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if ((uint32_t)p[j] < (uint64_t)rows) __builtin_memcpy(out + (long)p[j] * ldo + at, &v, sizeof(v));
+    }
+  }
+}
+
+// A token's places and weights, JB choices from j0 on, without branches: past
+// the last choice the last again, unused; a dropped pair reads row 0, unused.
+template <int JB>
+struct Choices {
+  long row[JB];
+  float w[JB];
+  bool use[JB];
+  DEV void load(const int32_t* pos, const float* wt, int j0, int k, long rows) {
+#pragma unroll
+    for (int j = 0; j < JB; ++j) {
+      const int jj = min(j0 + j, k - 1), p = pos[jj];
+      w[j] = wt ? wt[jj] : 1.0f;
+      use[j] = j0 + j < k && (uint32_t)p < (uint64_t)rows;
+      row[j] = use[j] ? p : 0;
+    }
+  }
+};
 
 // Weighted sum of a token's grouped rows in choice order, on top of base
-// (fp32, may be null); w null: weights of one.
-template <int DY, int DO, int V>
+// (fp32, may be null); w null: weights of one.  rows > 0.
+template <int DY, int DO, int V, int JB, bool WHOLE>
 __global__ void __launch_bounds__(256)
 unpermute_kernel(const typename Elem<DY>::type* __restrict__ y, long ldy, long rows, const int32_t* __restrict__ pos,
-                 const float* __restrict__ w, const float* base, long ldb, long T, int k, int units, RowMap m,
+                 const float* __restrict__ w, const float* base, long ldb, long T, int k, int cols, RowMap m,
                  typename Elem<DO>::type* out, long ldo) {
   long t;
-  const int u0 = row_of(m, t);
+  const int u0 = row_of<WHOLE>(m, t);
   if (t >= T) return;
-  for (int u = u0; u < units; u += 1 << m.tpr_log2) {
+  for (int c = u0 * V; c < cols; c += V << m.tpr_log2) {
+    const int at = min(c, cols - V);
     float acc[V];
     if (base) {
-      load_vals<MOE_T_F32, V>(base + t * ldb + (long)u * V, acc);
+      load_vals<MOE_T_F32, V>(base + t * ldb + at, acc);
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[i] = 0.0f;
     }
     for (int j0 = 0; j0 < k; j0 += JB) {
-      float v[JB][V], wj[JB];
-      bool use[JB];
+      Choices<JB> ch;
+      ch.load(pos + t * k, w ? w + t * k : nullptr, j0, k, rows);
+      float v[JB][V];
 #pragma unroll
-      for (int j = 0; j < JB; ++j) {
-        use[j] = false;
-        if (j0 + j >= k) continue;
-        const int p = pos[t * k + j0 + j];
-        use[j] = (uint32_t)p < (uint64_t)rows;
-        if (!use[j]) continue;
-        wj[j] = w ? w[t * k + j0 + j] : 1.0f;
-        load_vals<DY, V>(y + (long)p * ldy + (long)u * V, v[j]);
-      }
+      for (int j = 0; j < JB; ++j) load_vals<DY, V>(y + ch.row[j] * ldy + at, v[j]);
 #pragma unroll
       for (int j = 0; j < JB; ++j)
-        if (use[j])
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[i] = fmaf(wj[j], v[j][i], acc[i]);
+        for (int i = 0; i < V; ++i) acc[i] = ch.use[j] ? fmaf(ch.w[j], v[j][i], acc[i]) : acc[i];
     }
-    store_vals<DO, V>(out + t * ldo + (long)u * V, acc);
+    store_vals<DO, V>(out + t * ldo + at, acc);
   }
+}
+
+// No grouped rows at all: out = base, or zero.
+template <int DO>
+__global__ void __launch_bounds__(256)
+base_only_kernel(const float* base, long ldb, long n, int cols, typename Elem<DO>::type* out, long ldo) {
+  const long i = (long)blockIdx.x * 256 + threadIdx.x, t = i / cols;
+  if (t >= n) return;
+  const int c = (int)(i - t * cols);
+  out[t * ldo + c] = Elem<DO>::store(base ? base[t * ldb + c] : 0.0f);
 }
 
 // Gradients of unpermute: a token's dout values stay in registers while the
 // token's k rows are read (for dw) and their gradients stored.  dw's sum over
 // the row: per thread over its units, then a butterfly over the row's lanes,
 // then the row's waves in order.  Workgroups past the tokens zero dy's
-// padding rows.
-template <int DY, int DO, int V>
+// padding rows.  rows > 0.
+template <int DY, int DO, int V, int JB, bool WHOLE>
 __global__ void __launch_bounds__(256)
 unpermute_bwd_kernel(const typename Elem<DO>::type* __restrict__ dout, long ldd,
                      const typename Elem<DY>::type* __restrict__ y, long ldy, const int32_t* __restrict__ perm,
-                     long rows, const int32_t* __restrict__ pos, const float* __restrict__ w, long T, int k, int units,
+                     long rows, const int32_t* __restrict__ pos, const float* __restrict__ w, long T, int k, int cols,
                      unsigned tok_blocks, RowMap m, typename Elem<DY>::type* __restrict__ dy, long lddy,
                      float* __restrict__ dw) {
   if (blockIdx.x >= tok_blocks) {
@@ -358,47 +398,40 @@ unpermute_bwd_kernel(const typename Elem<DO>::type* __restrict__ dout, long ldd,
       const long r = r0 + i;
       if (r >= rows) return;
       if (perm[r] != -1) continue;
-      for (int u = threadIdx.x; u < units; u += 256) store_vals<DY, V>(dy + r * lddy + (long)u * V, zero);
+      for (int c = threadIdx.x * V; c < cols; c += 256 * V) store_vals<DY, V>(dy + r * lddy + min(c, cols - V), zero);
     }
     return;
   }
   __shared__ float part[4][JB];
   long t;
-  const int u0 = row_of(m, t);
+  const int u0 = row_of<WHOLE>(m, t);
   const bool live = t < T;
   const int tpr = 1 << m.tpr_log2;
   for (int j0 = 0; j0 < k; j0 += JB) {
-    float dot[JB], wj[JB];
-    int p[JB];
+    float dot[JB];
 #pragma unroll
-    for (int j = 0; j < JB; ++j) {
-      dot[j] = 0.0f;
-      p[j] = -1;
-      if (!live || j0 + j >= k) continue;
-      const int q = pos[t * k + j0 + j];
-      if ((uint32_t)q >= (uint64_t)rows) continue;
-      p[j] = q;
-      wj[j] = w[t * k + j0 + j];
-    }
-    if (live)
-      for (int u = u0; u < units; u += tpr) {
+    for (int j = 0; j < JB; ++j) dot[j] = 0.0f;
+    if (live) {
+      Choices<JB> ch;
+      ch.load(pos + t * k, w + t * k, j0, k, rows);
+      for (int c = u0 * V; c < cols; c += V * tpr) {
+        const int at = min(c, cols - V), again = c - at;        // values another unit has counted
         float g[V], v[JB][V];
-        load_vals<DO, V>(dout + t * ldd + (long)u * V, g);
+        load_vals<DO, V>(dout + t * ldd + at, g);
 #pragma unroll
-        for (int j = 0; j < JB; ++j)
-          if (p[j] >= 0) load_vals<DY, V>(y + (long)p[j] * ldy + (long)u * V, v[j]);
+        for (int j = 0; j < JB; ++j) load_vals<DY, V>(y + ch.row[j] * ldy + at, v[j]);
 #pragma unroll
-        for (int j = 0; j < JB; ++j)
-          if (p[j] >= 0) {
-            float o[V];
+        for (int j = 0; j < JB; ++j) {
+          float o[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-              dot[j] = fmaf(g[i], v[j][i], dot[j]);
-              o[i] = wj[j] * g[i];
-            }
-            store_vals<DY, V>(dy + (long)p[j] * lddy + (long)u * V, o);
+          for (int i = 0; i < V; ++i) {
+            dot[j] = ch.use[j] && i >= again ? fmaf(g[i], v[j][i], dot[j]) : dot[j];
+            o[i] = ch.w[j] * g[i];
           }
+          if (ch.use[j]) store_vals<DY, V>(dy + ch.row[j] * lddy + at, o);
+        }
       }
+    }
 #pragma unroll
     for (int j = 0; j < JB; ++j)
       for (int off = min(tpr, 64) >> 1; off >= 1; off >>= 1) dot[j] += __shfl_xor(dot[j], off, 64);
@@ -421,6 +454,11 @@ unpermute_bwd_kernel(const typename Elem<DO>::type* __restrict__ dout, long ldd,
         if (j0 + j < k) dw[t * k + j0 + j] = dot[j];
     }
   }
+}
+
+__global__ void __launch_bounds__(256) zero_kernel(float* p, long n) {
+  const long i = (long)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) p[i] = 0.0f;
 }
 
 // One wave per token: lane j holds choice j (k <= 64); every lane then sums
@@ -465,8 +503,6 @@ int launched() {
 
 int elem_bytes(int dt) { return dt == MOE_T_F32 ? 4 : (dt == MOE_T_BF16 || dt == MOE_T_F16 ? 2 : 0); }
 
-bool aligned16(const void* p, long ld, int bytes) { return ((uintptr_t)p | (uintptr_t)(ld * bytes)) % 16 == 0; }
-
 // Threads per row for `units` units, and the workgroups for T rows.
 RowMap row_map_for(int units, long T, long* blocks) {
   int l = 0;
@@ -488,43 +524,23 @@ int check_rows(int T, int k, int64_t rows, int cols) {
   return MOE_OK;
 }
 
-template <int DY, int DO, int V>
-int unpermute_as(const void* y, int64_t ldy, int64_t rows, const int32_t* pos, const float* w, const float* base,
-                 int64_t ldb, int T, int k, int cols, void* out, int64_t ldo, hipStream_t s) {
-  long blocks;
-  const RowMap m = row_map_for(cols / V, T, &blocks);
-  unpermute_kernel<DY, DO, V><<<(unsigned)blocks, 256, 0, s>>>((const typename Elem<DY>::type*)y, ldy, rows, pos, w,
-                                                               base, ldb, T, k, cols / V, m,
-                                                               (typename Elem<DO>::type*)out, ldo);
-  return launched();
-}
-
-template <int DY, int DO, int V>
-int unpermute_bwd_as(const void* dout, int64_t ldd, const void* y, int64_t ldy, const int32_t* perm, int64_t rows,
-                     const int32_t* pos, const float* w, int T, int k, int cols, void* dy, int64_t lddy, float* dw,
-                     hipStream_t s) {
-  long blocks;
-  const RowMap m = row_map_for(cols / V, T, &blocks);
-  const long pads = perm ? (rows + PAD_ROWS - 1) / PAD_ROWS : 0;
-  unpermute_bwd_kernel<DY, DO, V><<<(unsigned)(blocks + pads), 256, 0, s>>>(
-      (const typename Elem<DO>::type*)dout, ldd, (const typename Elem<DY>::type*)y, ldy, perm, rows, pos, w, T, k,
-      cols / V, (unsigned)blocks, m, (typename Elem<DY>::type*)dy, lddy, dw);
-  return launched();
-}
-
-// Calls f with compile-time types of the two rows and the values per access:
-// 16 bytes of the narrower type where every row starts on 16 bytes and the
-// width divides, else one.
+// f with compile-time types of the two rows, values per unit (one where a
+// row is narrower than a unit, or `single`) and choices in flight together.
 template <typename F>
-int by_types(int dy, int dout, bool wide, int cols, F f) {
-  const int V = dy == MOE_T_F32 && dout == MOE_T_F32 ? 4 : 8;
-  const bool vec = wide && cols % V == 0;
-#define CASE(A, B, W)                                                                  \
-  if (dy == A && dout == B)                                                            \
-    return vec ? f(std::integral_constant<int, A>(), std::integral_constant<int, B>(), \
-                   std::integral_constant<int, W>())                                   \
-               : f(std::integral_constant<int, A>(), std::integral_constant<int, B>(), \
-                   std::integral_constant<int, 1>());
+int by_types(int dy, int dout, bool single, int cols, int k, F f) {
+  const auto choices = [&](auto a, auto b, auto v) {
+    if (k == 1) return f(a, b, v, std::integral_constant<int, 1>());
+    if (k == 2) return f(a, b, v, std::integral_constant<int, 2>());
+    if (k <= 4) return f(a, b, v, std::integral_constant<int, 4>());
+    return f(a, b, v, std::integral_constant<int, 8>());
+  };
+#define CASE(A, B, W)                                                                                          \
+  if (dy == A && dout == B)                                                                                    \
+    return single || cols < W                                                                                  \
+               ? choices(std::integral_constant<int, A>(), std::integral_constant<int, B>(),                   \
+                         std::integral_constant<int, 1>())                                                     \
+               : choices(std::integral_constant<int, A>(), std::integral_constant<int, B>(),                   \
+                         std::integral_constant<int, W>());
   CASE(MOE_T_BF16, MOE_T_BF16, 8)
   CASE(MOE_T_F16, MOE_T_F16, 8)
   CASE(MOE_T_F32, MOE_T_F32, 4)
@@ -592,19 +608,23 @@ int moe_permute(int dtype, const void* x, int64_t ldx, const int32_t* perm, cons
   if (!out || (T && (!x || !pos))) return bad(MOE_E_INVAL, "null argument");
   const long pads = perm ? (rows + PAD_ROWS - 1) / PAD_ROWS : 0;
   const hipStream_t s = (hipStream_t)stream;
-  const long rowb = (long)cols * b;
-  const int unit = aligned16(x, ldx, b) && aligned16(out, ldo, b) && rowb % 16 == 0 ? 16 : b;
-  const int units = (int)(rowb / unit);
+  const int V = cols < 16 / b ? 1 : 16 / b;
   long blocks;
-  const RowMap m = row_map_for(units, T, &blocks);
+  const RowMap m = row_map_for((cols + V - 1) / V, T, &blocks);
   if (blocks + pads > MAX_BLOCKS) return bad(MOE_E_UNSUPPORTED, "too many rows");
   if (blocks + pads == 0) return MOE_OK;
-#define GO(U)                                                                                                   \
-  permute_kernel<U><<<(unsigned)(blocks + pads), 256, 0, s>>>((const U*)x, ldx * b / unit, pos, T, k, perm, rows, \
-                                                              units, (unsigned)blocks, m, (U*)out, ldo * b / unit)
-  if (unit == 16) GO(i32x4_t);
-  else if (unit == 4) GO(uint32_t);
-  else GO(uint16_t);
+#define GO(U, V, W)                                                                                               \
+  permute_kernel<U, V, W><<<(unsigned)(blocks + pads), 256, 0, s>>>((const U*)x, ldx, pos, T, k, perm, rows, cols, \
+                                                                    (unsigned)blocks, m, (U*)out, ldo)
+  if (b == 4) {
+    if (V == 1) GO(uint32_t, 1, false);
+    else if (m.tpr_log2 == 8) GO(uint32_t, 4, true);
+    else GO(uint32_t, 4, false);
+  } else {
+    if (V == 1) GO(uint16_t, 1, false);
+    else if (m.tpr_log2 == 8) GO(uint16_t, 8, true);
+    else GO(uint16_t, 8, false);
+  }
 #undef GO
   return launched();
 }
@@ -619,10 +639,26 @@ int moe_unpermute(int ytype, const void* y, int64_t ldy, int64_t rows, const int
   if (ldy < cols || ldo < cols || (base && ldb < cols)) return bad(MOE_E_INVAL, "row stride smaller than cols");
   if (T == 0) return MOE_OK;
   if ((rows && !y) || !pos || !out) return bad(MOE_E_INVAL, "null argument");
-  const bool wide = aligned16(y, ldy, by) && aligned16(out, ldo, bo) && (!base || aligned16(base, ldb, 4));
-  return by_types(ytype, otype, wide, cols, [&](auto a, auto o, auto v) {
-    return unpermute_as<a.value, o.value, v.value>(y, ldy, rows, pos, w, base, ldb, T, k, cols, out, ldo,
-                                                   (hipStream_t)stream);
+  const hipStream_t s = (hipStream_t)stream;
+  // in place a value may not be read and written twice
+  const bool single = base == out && cols % 8 != 0;
+  return by_types(ytype, otype, single, cols, k, [&](auto a, auto o, auto v, auto jb) {
+    typedef typename Elem<a.value>::type TY;
+    typedef typename Elem<o.value>::type TO;
+    if (rows == 0) {
+      base_only_kernel<o.value><<<(unsigned)(((long)T * cols + 255) / 256), 256, 0, s>>>(base, ldb, T, cols, (TO*)out,
+                                                                                       ldo);
+      return launched();
+    }
+    long blocks;
+    const RowMap m = row_map_for((cols + v.value - 1) / v.value, T, &blocks);
+    if (m.tpr_log2 == 8 && v.value > 1)
+      unpermute_kernel<a.value, o.value, v.value, jb.value, true><<<(unsigned)blocks, 256, 0, s>>>(
+          (const TY*)y, ldy, rows, pos, w, base, ldb, T, k, cols, m, (TO*)out, ldo);
+    else
+      unpermute_kernel<a.value, o.value, v.value, jb.value, false><<<(unsigned)blocks, 256, 0, s>>>(
+          (const TY*)y, ldy, rows, pos, w, base, ldb, T, k, cols, m, (TO*)out, ldo);
+    return launched();
   });
 }
 
@@ -636,10 +672,26 @@ int moe_unpermute_backward(int otype, const void* dout, int64_t ldd, int ytype, 
   if (ldd < cols || ldy < cols || lddy < cols) return bad(MOE_E_INVAL, "row stride smaller than cols");
   if (T == 0 && (rows == 0 || !perm)) return MOE_OK;
   if ((T && (!dout || !pos || !w || !dw)) || (rows && (!y || !dy))) return bad(MOE_E_INVAL, "null argument");
-  const bool wide = aligned16(y, ldy, by) && aligned16(dy, lddy, by) && aligned16(dout, ldd, bo);
-  return by_types(ytype, otype, wide, cols, [&](auto a, auto o, auto v) {
-    return unpermute_bwd_as<a.value, o.value, v.value>(dout, ldd, y, ldy, perm, rows, pos, w, T, k, cols, dy, lddy,
-                                                       dw, (hipStream_t)stream);
+  const hipStream_t s = (hipStream_t)stream;
+  return by_types(ytype, otype, false, cols, k, [&](auto a, auto o, auto v, auto jb) {
+    typedef typename Elem<a.value>::type TY;
+    typedef typename Elem<o.value>::type TO;
+    if (rows == 0) {
+      zero_kernel<<<(unsigned)(((long)T * k + 255) / 256), 256, 0, s>>>(dw, (long)T * k);
+      return launched();
+    }
+    long blocks;
+    const RowMap m = row_map_for((cols + v.value - 1) / v.value, T, &blocks);
+    const long pads = perm ? (rows + PAD_ROWS - 1) / PAD_ROWS : 0;
+    if (m.tpr_log2 == 8 && v.value > 1)
+      unpermute_bwd_kernel<a.value, o.value, v.value, jb.value, true><<<(unsigned)(blocks + pads), 256, 0, s>>>(
+          (const TO*)dout, ldd, (const TY*)y, ldy, perm, rows, pos, w, T, k, cols, (unsigned)blocks, m, (TY*)dy, lddy,
+          dw);
+    else
+      unpermute_bwd_kernel<a.value, o.value, v.value, jb.value, false><<<(unsigned)(blocks + pads), 256, 0, s>>>(
+          (const TO*)dout, ldd, (const TY*)y, ldy, perm, rows, pos, w, T, k, cols, (unsigned)blocks, m, (TY*)dy, lddy,
+          dw);
+    return launched();
   });
 }
 
