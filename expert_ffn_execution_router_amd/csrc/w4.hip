@@ -312,7 +312,8 @@ w4_kernel(W4Args a, int otype, int blocks, int per, int passes) {
     };
     int first = t0;
     asm volatile("" : "+s"(first));             // its addresses are not kept over the blocks
-    if (!LONG) load(first);
+    if (LONG) place(0);
+    load(first);
     frag x[S][4];
     f32x4_t kept[KEEP ? S : 1][SUB];
     const uint16_t* xr = x_row(a, r0 + l, r_end);
@@ -385,16 +386,20 @@ w4_kernel(W4Args a, int otype, int blocks, int per, int passes) {
       if (!LONG) {
         multiply();
       } else {
-        for (int p = 0; p < passes; ++p) {
-          place(p);
-          load(tile0);
+        for (int p = 0;;) {
           load_x(p);
           multiply();
+          if (++p == passes) break;
+          place(p);
+          load(tile0);
         }
       }
       const int tile1 = tile0 + NO;
       const bool more = tile1 < t_end;
-      if (!LONG && more) load(tile1);
+      if (more) {
+        if (LONG) place(0);
+        load(tile1);
+      }
       if (4 * g < rows)
 #pragma unroll
         for (int q = 0; q < NR; ++q) *(f32x4_t*)(red + (((wave * NR + q) << ql) + g) * 64 + 4 * l) = total[q];
@@ -450,15 +455,20 @@ void launch(const W4Args& a, int otype, hipStream_t s) {
       a, otype, (int)blocks, (int)per, passes);
 }
 
-// Steps of inputs per wave: as few as let eight waves hold a row, 2 at least
-// (their group values come in pairs); past 64 steps a row is taken in passes.
+// Two steps of inputs per wave (their group values come in pairs) hold rows of
+// up to 2048; longer rows are taken in passes, the x rows read again for each
+// tile pair: 4096 inputs, 16 rows, 4096 weight rows 9.1 us against 9.9 with
+// four steps held, 6144 inputs, 64 rows, 12288 gated rows 56 against 74 with
+// six (twice the registers, half the waves).  With thousands of pairs holding
+// four steps wins back the x reads: 64 experts, 4096 inputs, 4096 rows 110
+// against 140 us.
 template <int XT, int ST, int GM, bool GATED, bool HZ>
 void choose(const W4Args& a, int otype, hipStream_t s) {
   const int steps = (a.K + 127) / 128;
-  if (steps <= 16) launch<XT, ST, GM, 2, false, GATED, HZ>(a, otype, s);
-  else if (steps <= 32) launch<XT, ST, GM, 4, false, GATED, HZ>(a, otype, s);
-  else if (steps <= 48) launch<XT, ST, GM, 6, false, GATED, HZ>(a, otype, s);
-  else launch<XT, ST, GM, 4, true, GATED, HZ>(a, otype, s);
+  const long pairs = (((GATED ? a.N / 2 : a.N) + 15) / 16 + (GATED ? 0 : 1)) / (GATED ? 1 : 2) * row_blocks(a);
+  if (steps <= 2 * MAX_WAVES) launch<XT, ST, GM, 2, false, GATED, HZ>(a, otype, s);
+  else if (steps <= 4 * MAX_WAVES && pairs >= 4096) launch<XT, ST, GM, 4, false, GATED, HZ>(a, otype, s);
+  else launch<XT, ST, GM, 2, true, GATED, HZ>(a, otype, s);
 }
 
 template <int XT, int ST, bool GATED, bool HZ>
