@@ -14,6 +14,7 @@ F32_ONLY = {torch.float32: B.MOE_T_F32}
 BYTES = {B.MOE_T_BF16: 2, B.MOE_T_F16: 2, B.MOE_T_F32: 4}
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def rows(name, t, dev, n, cols, types=TYPES):
@@ -66,7 +67,7 @@ def launch(fn, dev, stream, *args):
         raise ValueError(f"stream of {stream.device}, tensors on device {dev}")
     else:
         s = stream.cuda_stream
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         rc = fn(*args, s)
     else:
         with torch.cuda.device(dev):

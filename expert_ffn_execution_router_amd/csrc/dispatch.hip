@@ -511,7 +511,7 @@ RowMap row_map_for(int units, long T, long* blocks) {
   return RowMap{l};
 }
 
-constexpr long MAX_BLOCKS = 0x7fffffffL;
+constexpr long MAX_BLOCKS = (1L << 24) - 1;     // of 256 threads: a launch holds fewer than 2^32
 constexpr int MAX_K = 64;
 
 long sort_blocks(long n) { return n <= SORT_SPAN ? 1 : (n + SORT_SPAN - 1) / SORT_SPAN; }
@@ -521,6 +521,7 @@ int check_rows(int T, int k, int64_t rows, int cols) {
   if ((int64_t)T * k > 0x7fffffffLL) return bad(MOE_E_UNSUPPORTED, "more than 2^31 - 1 pairs");
   if (rows < 0 || rows > 0x7fffffffLL) return bad(MOE_E_INVAL, "rows outside [0, 2^31)");
   if (cols < 1) return bad(MOE_E_INVAL, "need cols >= 1");
+  if (cols > 1 << 30) return bad(MOE_E_UNSUPPORTED, "rows wider than 2^30");
   return MOE_OK;
 }
 
@@ -639,6 +640,8 @@ int moe_unpermute(int ytype, const void* y, int64_t ldy, int64_t rows, const int
   if (ldy < cols || ldo < cols || (base && ldb < cols)) return bad(MOE_E_INVAL, "row stride smaller than cols");
   if (T == 0) return MOE_OK;
   if ((rows && !y) || !pos || !out) return bad(MOE_E_INVAL, "null argument");
+  if (base == out && (otype != MOE_T_F32 || ldb != ldo)) return bad(MOE_E_INVAL, "base is out: fp32, of one stride");
+  if (rows == 0 && ((long)T * cols + 255) / 256 > MAX_BLOCKS) return bad(MOE_E_UNSUPPORTED, "too many values");
   const hipStream_t s = (hipStream_t)stream;
   // in place a value may not be read and written twice
   const bool single = base == out && cols % 8 != 0;
@@ -652,6 +655,7 @@ int moe_unpermute(int ytype, const void* y, int64_t ldy, int64_t rows, const int
     }
     long blocks;
     const RowMap m = row_map_for((cols + v.value - 1) / v.value, T, &blocks);
+    if (blocks > MAX_BLOCKS) return bad(MOE_E_UNSUPPORTED, "too many rows");
     if (m.tpr_log2 == 8 && v.value > 1)
       unpermute_kernel<a.value, o.value, v.value, jb.value, true><<<(unsigned)blocks, 256, 0, s>>>(
           (const TY*)y, ldy, rows, pos, w, base, ldb, T, k, cols, m, (TO*)out, ldo);
@@ -683,6 +687,7 @@ int moe_unpermute_backward(int otype, const void* dout, int64_t ldd, int ytype, 
     long blocks;
     const RowMap m = row_map_for((cols + v.value - 1) / v.value, T, &blocks);
     const long pads = perm ? (rows + PAD_ROWS - 1) / PAD_ROWS : 0;
+    if (blocks + pads > MAX_BLOCKS) return bad(MOE_E_UNSUPPORTED, "too many rows");
     if (m.tpr_log2 == 8 && v.value > 1)
       unpermute_bwd_kernel<a.value, o.value, v.value, jb.value, true><<<(unsigned)(blocks + pads), 256, 0, s>>>(
           (const TO*)dout, ldd, (const TY*)y, ldy, perm, rows, pos, w, T, k, cols, (unsigned)blocks, m, (TY*)dy, lddy,
@@ -702,6 +707,7 @@ int moe_gate_backward(const int32_t* ids, const float* w, const float* dw, int T
   if (E < 1 || ldz < E) return bad(MOE_E_INVAL, "need E >= 1 and a row stride of at least E");
   if (T == 0) return MOE_OK;
   if (!ids || !w || !dw || !dz) return bad(MOE_E_INVAL, "null argument");
+  if ((T + 3L) / 4 > MAX_BLOCKS) return bad(MOE_E_UNSUPPORTED, "too many tokens");
   gate_bwd_kernel<<<(unsigned)((T + 3L) / 4), 256, 0, (hipStream_t)stream>>>(ids, w, dw, T, k, E, dz, ldz);
   return launched();
 }

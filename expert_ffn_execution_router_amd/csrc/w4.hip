@@ -82,16 +82,11 @@ struct Frag<MOE_T_F16> {
 };
 
 // The 8 codes of a word (two per byte, even input in the low nibble) as 8
-// integers, in input order or (PLAIN = false, two instructions fewer) the
-// even inputs before the odd ones.
-template <int XT, bool PLAIN>
+// integers, the even inputs before the odd ones (input order costs two
+// instructions more; the x rows are put in this order once instead).
+template <int XT>
 DEV typename Frag<XT>::type codes8(uint32_t w) {
-  uint32_t a = w & 0x0F0F0F0Fu, b = (w >> 4) & 0x0F0F0F0Fu;
-  if (PLAIN) {
-    const uint32_t even = a, odd = b;
-    a = __builtin_amdgcn_perm(odd, even, 0x05010400u);
-    b = __builtin_amdgcn_perm(odd, even, 0x07030602u);
-  }
+  const uint32_t a = w & 0x0F0F0F0Fu, b = (w >> 4) & 0x0F0F0F0Fu;
   const i32x4_t v = {(int)Frag<XT>::lo(a), (int)Frag<XT>::hi(a), (int)Frag<XT>::lo(b), (int)Frag<XT>::hi(b)};
   return __builtin_bit_cast(typename Frag<XT>::type, v);
 }
@@ -171,7 +166,7 @@ long row_blocks(const W4Args& a) {
 
 // What rows without an x row read.
 constexpr int MAX_K = 32768;
-__device__ uint16_t w4_zeros[MAX_K];
+alignas(16) __device__ uint16_t w4_zeros[MAX_K];
 
 // The x row that grouped row r reads, zeros if there is none; r not below end
 // reads the last row's (for result rows that are not stored).
@@ -372,7 +367,7 @@ w4_kernel(W4Args a, int otype, int blocks, int per, int passes) {
               f32x4_t c = HZ ? f32x4_t{0.0f, 0.0f, 0.0f, 0.0f} : xsum;
 #pragma unroll
               for (int j = h * PER; j < (h + 1) * PER; ++j)
-                c = Frag<XT>::mfma(x[s][j], codes8<XT, false>((uint32_t)c4[q][j]), c);
+                c = Frag<XT>::mfma(x[s][j], codes8<XT>((uint32_t)c4[q][j]), c);
 #pragma unroll
               for (int j = 0; j < 4; ++j) total[q][j] = fmaf(sf, HZ ? fmaf(-zf, xsum[j], c[j]) : c[j], total[q][j]);
             }
@@ -501,6 +496,7 @@ extern "C" int moe_w4_matmul(int xtype, const void* x, int64_t ldx, int64_t x_ro
   if (K > MAX_K) return bad(MOE_E_UNSUPPORTED, "K over 32768");
   if (rows < 0 || rows > 0x7fffffffLL || x_rows < 0) return bad(MOE_E_INVAL, "rows outside [0, 2^31)");
   if (E < 1 || E > 1024) return bad(MOE_E_INVAL, "need 1 <= E <= 1024");
+  if ((int64_t)N * (K / group) > (1 << 30)) return bad(MOE_E_UNSUPPORTED, "more than 2^30 groups in a matrix");
   if (K != group && (int64_t)E * N * (K / group) < 4) return bad(MOE_E_UNSUPPORTED, "fewer than 4 groups in all");
   if (!offsets && (E != 1 || counts)) return bad(MOE_E_INVAL, "without offsets: one matrix and no counts");
   if (row_map && map_div < 1) return bad(MOE_E_INVAL, "need map_div >= 1");
@@ -514,8 +510,7 @@ extern "C" int moe_w4_matmul(int xtype, const void* x, int64_t ldx, int64_t x_ro
            (const uint16_t*)zeros, N, K, K / group, 0, out, ldo};
   const uint32_t runs = group < 128 ? 1 : group / 128;      // a step never passes a group of more than 128
   a.per_group = ((1u << 31) + runs - 1) / runs;
-
-    const hipStream_t s = (hipStream_t)stream;
+  const hipStream_t s = (hipStream_t)stream;
   constexpr int BF = MOE_T_BF16, HF = MOE_T_F16;
   if (xtype == BF) stype == BF ? choose_form<BF, BF>(a, gated, otype, s) : choose_form<BF, HF>(a, gated, otype, s);
   else stype == BF ? choose_form<HF, BF>(a, gated, otype, s) : choose_form<HF, HF>(a, gated, otype, s);

@@ -6,7 +6,9 @@ int32 [T, k] with ids outside [0, E) dropped; counts, offsets, perm and pos
 are what sort() writes (moe_sort in include/moe.h has their meaning).  Hidden
 rows are bf16, fp16 or fp32 [rows, cols] views with contiguous rows.  Calls
 enqueue on the current stream of the tensors' device (or `stream`, which the
-caller orders after the work that made the inputs) and can be captured.
+caller orders after the work that made the inputs) and can be captured.  The
+memory from a result's first to its last value must not meet an input's,
+except for unpermute's base in place.
 
 A forward and backward of the experts' surroundings:
 
@@ -112,7 +114,8 @@ def permute_backward(dout, pos, dx, stream=None):
 def unpermute_backward(dout, y, perm, pos, w, dy, dw, stream=None):
     """Gradients of unpermute: dy[pos[t, j]] = w[t, j] dout[t] and dw[t, j] =
     <dout[t], y[pos[t, j]]> (0 for dropped pairs).  Padding rows of dy become
-    zero (perm None: there are none), rows behind the last segment stay."""
+    zero (perm None: there are none), rows behind the last segment stay.  After
+an unpermute without weights dy is permute(dout)."""
     dev, cols, n = y.get_device(), y.shape[-1], y.shape[0]
     pp, shape = _tokens("pos", pos, dev)
     T, k = shape

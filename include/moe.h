@@ -463,7 +463,8 @@ int moe_profile_end(moe_ctx* ctx, moe_profile* out);
  * with 4-bit weights.  No context; every pointer is device memory; sizes,
  * types and strides are checked on the host before any device work (message
  * in moe_last_error(NULL)).  Rows have a stride (ld*, in elements, at least
- * the width) and contiguous values.  Calls only enqueue kernels on stream, so
+ * the width) and contiguous values.  No output shares memory with an input,
+ * but for moe_unpermute's base.  Calls only enqueue kernels on stream, so
  * they can be captured, and they keep nothing between calls: calls on
  * different streams are independent as long as their outputs and workspaces
  * are.  Equal inputs give equal bits.  T = 0 and rows = 0 are valid.
@@ -490,8 +491,9 @@ int moe_sort(const int32_t* ids, int T, int k, int E, int align, int32_t* counts
 /* Token rows to their grouped places: out[pos[t,j]] = x[t], for each pair
  * with 0 <= pos < rows.  x [T, cols], out [rows, cols] of one MOE_T_* type.
  * perm (may be NULL: no padding): rows with perm = -1 are set to zero; rows
- * behind the last segment are left as they were.  The gradient of this call
- * is moe_unpermute without weights. */
+ * behind the last segment are left as they were.  pos as moe_sort gives it: no
+ * row twice, here and in moe_unpermute_backward, which store by it.  The
+ * gradient of this call is moe_unpermute without weights. */
 int moe_permute(int dtype, const void* x, int64_t ldx, const int32_t* perm, const int32_t* pos, int T, int k,
                 int64_t rows, int cols, void* out, int64_t ldo, void* stream);
 
@@ -499,8 +501,8 @@ int moe_permute(int dtype, const void* x, int64_t ldx, const int32_t* perm, cons
  * over the pairs with 0 <= pos < rows, fp32 sums in choice order on top of
  * base, rounded once.  y [rows, cols]; w fp32 [T, k], or NULL for ones; base
  * fp32 [T, cols] or NULL for zero (a host partial, a shared expert's output;
- * it may be out itself when out is fp32).  A token whose pairs are all
- * dropped gets base.  Types: equal, or one of y and out fp32. */
+ * it may be out itself, of the same stride, when out is fp32).  A token whose
+ * pairs are all dropped gets base.  Types: equal, or one of y and out fp32. */
 int moe_unpermute(int ytype, const void* y, int64_t ldy, int64_t rows, const int32_t* pos, const float* w,
                   const float* base, int64_t ldb, int T, int k, int cols, int otype, void* out, int64_t ldo,
                   void* stream);
@@ -531,7 +533,8 @@ int moe_gate_backward(const int32_t* ids, const float* w, const float* dw, int T
  * gated != 0: the matrix is [gate; up] stacked (N even) and
  * out[r] = silu(z[r, :N/2]) * z[r, N/2:], [rows, N/2]; else out [rows, N].
  * x bf16 or fp16 [x_rows, K], on 16 bytes, stride a multiple of 8, finite (a
- * row with an infinity or NaN gives NaN, other rows are not touched by it).
+ * row with an infinity or NaN gives NaN, other rows are not touched by it);
+ * scales and zeros finite.
  *   dense (offsets NULL, E = 1): out row r from x row r.
  *   per expert: grouped rows offsets[e] .. + counts[e] (counts NULL: up to
  *     offsets[e+1]) use matrix e; offsets int32 [E+1], counts int32 [E] as
@@ -540,8 +543,8 @@ int moe_gate_backward(const int32_t* ids, const float* w, const float* dw, int T
  *     row_map[r] / map_div (moe_sort's perm with map_div = k reads token
  *     rows); a map entry outside x reads a row of zeros.
  * Any number of rows is valid; the design point is up to 64 per matrix.
- * E <= 1024, K <= 32768, at least 4 groups in all unless group = K.  INVAL,
- * UNSUPPORTED, HIP. */
+ * E <= 1024, K <= 32768, N * K / group <= 2^30, at least 4 groups in all
+ * unless group = K.  INVAL, UNSUPPORTED, HIP. */
 int moe_w4_matmul(int xtype, const void* x, int64_t ldx, int64_t x_rows, const int32_t* row_map, int map_div,
                   const int32_t* offsets, const int32_t* counts, int E, int64_t rows, const uint8_t* codes, int stype,
                   const void* scales, const void* zeros, int N, int K, int group, int gated, int otype, void* out,

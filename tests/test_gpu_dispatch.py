@@ -157,6 +157,60 @@ def test_unpermute_base_in_place():
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("yt", [BF, F32])
+@pytest.mark.parametrize("cols", [5, 9, 12, 513, 4100])
+def test_base_in_place_of_odd_widths(cols, yt):
+    """Units that overlap would add a value's rows twice."""
+    print(f"in place cols={cols} {yt}", flush=True)
+    rng = np.random.default_rng(cols)
+    ids, perm, pos = plan(21, 3, 7, 4, 0.2, 4)
+    y = poisoned_rows(rng, perm, cols, yt, 1, 0)
+    w = torch.from_numpy(rng.random((21, 3)).astype(np.float32)).cuda()
+    a = torch.randn(21, cols + 3, device="cuda")[:, :cols]
+    b = torch.empty(21, cols, device="cuda")
+    D.unpermute(y, pos, w, b, base=a)
+    D.unpermute(y, pos, w, a, base=a)
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_no_tokens_still_clear_padding(dt):
+    print(f"no tokens {dt}", flush=True)
+    perm = torch.tensor([-1, -2, -1] + [-2] * 40 + [-1], dtype=torch.int32, device="cuda")
+    pos, w = torch.zeros(0, 2, dtype=torch.int32, device="cuda"), torch.zeros(0, 2, device="cuda")
+    x, want = torch.zeros(0, 67, device="cuda", dtype=dt), torch.full((44, 67), 5.0, device="cuda", dtype=dt)
+    out, y = want.clone(), want.clone()
+    want[perm == -1] = 0
+    D.permute(x, perm, pos, out)
+    assert torch.equal(out, want)
+    dy = torch.full_like(want, 5.0)
+    D.unpermute_backward(x, y, perm, pos, w, dy, w.clone())
+    assert torch.equal(dy, want)
+
+
+def test_offsets_past_32_bits():
+    """Rows 2^30 values apart, in each role."""
+    print("rows far apart", flush=True)
+    cols, far = 264, 2 ** 30
+    ids, perm, pos = plan(5, 1, 3, 1, 0.0, 5, extra=0)
+    wide = [torch.empty(5, far, device="cuda", dtype=BF)[:, 8:8 + cols] for _ in range(3)]
+    x, xs, dy = wide
+    x.copy_(torch.randn(5, cols, device="cuda"))
+    D.permute(x, perm, pos, xs)
+    near, nxs = x.contiguous(), torch.zeros(5, cols, device="cuda", dtype=BF)
+    D.permute(near, perm, pos, nxs)
+    assert torch.equal(xs, nxs) and torch.equal(nxs[pos[:, 0].long()], near)
+    w = torch.rand(5, 1, device="cuda")
+    ndy, dw, ndw = torch.zeros_like(nxs), torch.zeros(5, 1, device="cuda"), torch.zeros(5, 1, device="cuda")
+    D.unpermute_backward(x, xs, perm, pos, w, dy, dw)
+    D.unpermute_backward(near, nxs, perm, pos, w, ndy, ndw)
+    assert torch.equal(dy, ndy) and torch.equal(dw, ndw)
+    out = torch.zeros(5, cols, device="cuda", dtype=BF)
+    D.unpermute(xs, pos, w, x)
+    D.unpermute(nxs, pos, w, out)
+    assert torch.equal(x, out)
+
+
 @pytest.mark.parametrize("yt,ot", PAIRS)
 @pytest.mark.parametrize("T,k,E,cols,align,drop,pad,shift", SHAPES)
 def test_unpermute_backward(T, k, E, cols, align, drop, pad, shift, yt, ot):

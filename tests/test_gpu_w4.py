@@ -198,6 +198,44 @@ def test_experts_map_outside_reads_zeros():
     check(out[[0, 3]], np64(x)[[2, 0]], q[0], s[0], z[0], 32, False)
 
 
+def test_experts_past_32_bits():
+    """Codes of the last experts lie past 4 GiB, their rows and results past
+    2^31 values."""
+    print("experts past 32 bits", flush=True)
+    rng = np.random.default_rng(8)
+    E, N, K, group, far = 70, 8192, 16384, 512, 2 ** 30
+    codes = torch.randint(0, 256, (E, N, K // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.rand(E, N, K // group, device="cuda").mul_(0.01).to(BF)
+    x = torch.empty(5, far, device="cuda", dtype=BF)[:, :K]
+    x.copy_(xrows(rng, 5, K, BF))
+    out = torch.empty(5, far, device="cuda", dtype=BF)[:, :N]
+    o = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    o[35:], o[69:], o[70:] = 1, 2, 5
+    w4.experts(x, o, out, codes, scales)
+    for e, r in ((34, [0]), (68, [1]), (69, [2, 3, 4])):
+        n = torch.tensor([0, 1, 777, 4096, N - 1], device="cuda")
+        b = codes[e][n].cpu().numpy()
+        q = np.stack([b & 15, b >> 4], -1).reshape(len(n), K)
+        check(out[r][:, n], np64(x[r]), q, np64(scales[e][n]), None, group, False)
+
+
+def test_two_streams_at_once():
+    """Two products of different weights in flight together, each on its own
+    stream."""
+    print("two streams", flush=True)
+    rng = np.random.default_rng(9)
+    todo = []
+    for i in range(2):
+        dev, host = matrix(rng, (130,), 6144, 64, BF, BF, i == 1)
+        todo.append((torch.cuda.Stream(), xrows(rng, 7 + i, 6144, BF), torch.zeros(7 + i, 130, device="cuda"), dev, host))
+    torch.cuda.synchronize()
+    for s, x, out, dev, _ in todo:
+        w4.linear(x, out, *dev, stream=s)
+    torch.cuda.synchronize()
+    for _, x, out, _, host in todo:
+        check(out, np64(x), *host, 64, False)
+
+
 def layer(b):
     """A MoE layer on 4-bit experts with a gated shared expert."""
     D.sort(b["ids"], b["counts"], b["offsets"], b["perm"], b["pos"])

@@ -65,10 +65,20 @@ def test_row_refusals(B):
                 dict(rows=-1), dict(x=None), dict(pos=None), dict(out=None)):
         assert permute(**bad) == B.MOE_E_INVAL, bad
     assert permute(rows=0) == 0
+    wide = 2 ** 30 + 1
+    assert permute(cols=wide, ldx=wide, ldo=wide) == B.MOE_E_UNSUPPORTED
+    many = dict(T=2 ** 24, k=1, cols=4096)
+    assert permute(ldx=4096, ldo=4096, **many) == B.MOE_E_UNSUPPORTED      # over 2^24 - 1 workgroups
+    assert unpermute(ldy=4096, ldo=4096, **many) == B.MOE_E_UNSUPPORTED
+    assert unpermute(ldy=4096, ldo=4096, rows=0, **many) == B.MOE_E_UNSUPPORTED
+    assert backward(ldd=4096, ldy=4096, lddy=4096, **many) == B.MOE_E_UNSUPPORTED
+    assert gate(T=2 ** 26, k=1) == B.MOE_E_UNSUPPORTED
     for bad in (dict(yt=3), dict(ot=9), dict(ldy=63), dict(ldo=1), dict(base=P, ldb=63), dict(T=-1), dict(k=0),
                 dict(cols=0), dict(rows=-1), dict(y=None), dict(pos=None), dict(out=None)):
         assert unpermute(**bad) == B.MOE_E_INVAL, bad
     assert unpermute(yt=0, ot=1) == B.MOE_E_UNSUPPORTED
+    assert unpermute(base=P, ldb=64) == B.MOE_E_INVAL                      # out itself, but bf16
+    assert unpermute(ot=2, base=P, ldb=72, ldo=64) == B.MOE_E_INVAL        # out itself, of another stride
     assert unpermute(T=0) == 0
     for bad in (dict(yt=3), dict(ot=9), dict(ldy=63), dict(ldd=1), dict(lddy=63), dict(T=-1), dict(k=65),
                 dict(cols=0), dict(rows=-1), dict(y=None), dict(pos=None), dict(dout=None), dict(dy=None),
@@ -96,6 +106,7 @@ def test_w4_refusals(B):
         assert mm(**bad) == B.MOE_E_INVAL, bad
     assert mm(K=32896, ldx=32896) == B.MOE_E_UNSUPPORTED
     assert mm(N=1, K=64, group=32, ldx=64) == B.MOE_E_UNSUPPORTED          # fewer than 4 groups in all
+    assert mm(N=2 ** 28, group=32, ldo=2 ** 28) == B.MOE_E_UNSUPPORTED
     assert mm(rows=0) == 0
 
 
