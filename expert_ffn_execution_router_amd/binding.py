@@ -114,15 +114,17 @@ SIGNATURES = {
     "moe_check_device_error": (_i, [_vp]),
     "moe_profile_begin": (_i, [_vp, _i, ctypes.c_uint]),
     "moe_profile_end": (_i, [_vp, _P(moe_profile)]),
-    "moe_sort_rows": (_ll, [_i, _i, _i, _i]),
-    "moe_sort_workspace_bytes": (_sz, [_i, _i, _i]),
-    "moe_sort": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _vp, _ll, _vp, _vp, _sz, _vp]),
-    "moe_permute": (_i, [_i, _vp, _ll, _vp, _vp, _i, _i, _ll, _i, _vp, _ll, _vp]),
-    "moe_unpermute": (_i, [_i, _vp, _ll, _ll, _vp, _vp, _vp, _ll, _i, _i, _i, _i, _vp, _ll, _vp]),
-    "moe_unpermute_backward": (_i, [_i, _vp, _ll, _i, _vp, _ll, _vp, _ll, _vp, _vp, _i, _i, _i, _vp, _ll, _vp, _vp]),
-    "moe_gate_backward": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _ll, _vp]),
-    "moe_w4_matmul": (_i, [_i, _vp, _ll, _ll, _vp, _i, _vp, _vp, _i, _ll, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _vp,
-                           _ll, _vp]),
+    # sizes of these are 64 bits: ctypes cuts a larger int to a c_int without an error
+    "moe_sort_rows": (_ll, [_ll, _ll, _ll, _ll]),
+    "moe_sort_workspace_bytes": (_sz, [_ll, _ll, _ll]),
+    "moe_sort": (_i, [_vp, _ll, _ll, _ll, _ll, _vp, _vp, _vp, _ll, _vp, _vp, _sz, _vp]),
+    "moe_permute": (_i, [_i, _vp, _ll, _vp, _vp, _ll, _ll, _ll, _ll, _vp, _ll, _vp]),
+    "moe_unpermute": (_i, [_i, _vp, _ll, _ll, _vp, _vp, _vp, _ll, _ll, _ll, _ll, _i, _vp, _ll, _vp]),
+    "moe_unpermute_backward": (_i, [_i, _vp, _ll, _i, _vp, _ll, _vp, _ll, _vp, _vp, _ll, _ll, _ll, _vp, _ll, _vp,
+                                    _vp]),
+    "moe_gate_backward": (_i, [_vp, _vp, _vp, _ll, _ll, _ll, _vp, _ll, _vp]),
+    "moe_w4_matmul": (_i, [_i, _vp, _ll, _ll, _vp, _ll, _vp, _vp, _ll, _ll, _vp, _i, _vp, _vp, _ll, _ll, _ll, _i, _i,
+                           _vp, _ll, _vp]),
 }
 
 _lib = None

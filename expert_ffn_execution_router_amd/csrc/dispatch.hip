@@ -516,13 +516,16 @@ RowMap row_map_for(int units, long T, long* blocks) {
 
 constexpr long MAX_BLOCKS = (1L << 24) - 1;     // of 256 threads: a launch holds fewer than 2^32
 constexpr int MAX_K = 64;
+constexpr int64_t I32_MAX = 0x7fffffff;
 
 long sort_blocks(long n) { return n <= SORT_SPAN ? 1 : (n + SORT_SPAN - 1) / SORT_SPAN; }
 
-int check_rows(int T, int k, int64_t rows, int cols) {
+// Sizes come in 64 bits, so that none is cut to 32 before it is checked; what
+// passes here fits an int.
+int check_rows(int64_t T, int64_t k, int64_t rows, int64_t cols) {
   if (T < 0 || k < 1 || k > MAX_K) return bad(MOE_E_INVAL, "need T >= 0 and 1 <= k <= 64");
-  if ((int64_t)T * k > 0x7fffffffLL) return bad(MOE_E_UNSUPPORTED, "more than 2^31 - 1 pairs");
-  if (rows < 0 || rows > 0x7fffffffLL) return bad(MOE_E_INVAL, "rows outside [0, 2^31)");
+  if (T > I32_MAX || T * k > I32_MAX) return bad(MOE_E_UNSUPPORTED, "more than 2^31 - 1 pairs");
+  if (rows < 0 || rows > I32_MAX) return bad(MOE_E_INVAL, "rows outside [0, 2^31)");
   if (cols < 1) return bad(MOE_E_INVAL, "need cols >= 1");
   if (cols > 1 << 30) return bad(MOE_E_UNSUPPORTED, "rows wider than 2^30");
   return MOE_OK;
@@ -560,25 +563,27 @@ int by_types(int dy, int dout, bool single, int cols, int k, F f) {
 
 extern "C" {
 
-int64_t moe_sort_rows(int T, int k, int E, int align) {
+int64_t moe_sort_rows(int64_t T, int64_t k, int64_t E, int64_t align) {
   if (T < 0 || k < 1 || E < 1 || align < 1) return -1;
-  const int64_t n = (int64_t)T * k;
-  return n + (n < E ? n : E) * (int64_t)(align - 1);
+  if (T > I32_MAX || k > I32_MAX || E > I32_MAX || align > I32_MAX) return -1;      // sums below fit 64 bits
+  const int64_t n = T * k;
+  return n + (n < E ? n : E) * (align - 1);
 }
 
-size_t moe_sort_workspace_bytes(int T, int k, int E) {
-  if (T < 0 || k < 1 || E < 1) return 0;
-  const long nb = sort_blocks((long)T * k);
+size_t moe_sort_workspace_bytes(int64_t T, int64_t k, int64_t E) {
+  if (T < 0 || k < 1 || E < 1 || T > I32_MAX || k > I32_MAX || E > I32_MAX) return 0;
+  const long nb = sort_blocks(T * k);
   return nb == 1 ? 0 : (size_t)(nb + 1) * E * 4;
 }
 
-int moe_sort(const int32_t* ids, int T, int k, int E, int align, int32_t* counts, int32_t* offsets, int32_t* perm,
-             int64_t rows, int32_t* pos, void* ws, size_t ws_bytes, void* stream) {
+int moe_sort(const int32_t* ids, int64_t T, int64_t k, int64_t E, int64_t align, int32_t* counts, int32_t* offsets,
+             int32_t* perm, int64_t rows, int32_t* pos, void* ws, size_t ws_bytes, void* stream) {
   int rc = check_rows(T, k, rows, 1);
   if (rc) return rc;
-  if (E < 1 || E > SORT_MAX_E || align < 1) return bad(MOE_E_INVAL, "need 1 <= E <= 1024 and align >= 1");
+  if (E < 1 || E > SORT_MAX_E || align < 1 || align > I32_MAX)
+    return bad(MOE_E_INVAL, "need 1 <= E <= 1024 and 1 <= align < 2^31");
   if (rows < moe_sort_rows(T, k, E, align)) return bad(MOE_E_INVAL, "perm holds fewer rows than moe_sort_rows");
-  const long n = (long)T * k;
+  const long n = T * k;
   if (!counts || !offsets || (n && (!ids || !pos)) || (rows && !perm)) return bad(MOE_E_INVAL, "null argument");
   const size_t need = moe_sort_workspace_bytes(T, k, E);
   if (need && (!ws || ws_bytes < need)) return bad(MOE_E_INVAL, "workspace smaller than moe_sort_workspace_bytes");
@@ -595,14 +600,14 @@ int moe_sort(const int32_t* ids, int T, int k, int E, int align, int32_t* counts
   }
   int32_t* hist = (int32_t*)ws;
   sort_hist_kernel<<<(unsigned)nb, SORT_THREADS, (size_t)E * 4, s>>>(ids, n, E, hist);
-  sort_scan_kernel<<<(E + 63) / 64, 1024, 0, s>>>(hist, (int)nb, E);
+  sort_scan_kernel<<<(unsigned)((E + 63) / 64), 1024, 0, s>>>(hist, (int)nb, E);
   sort_kernel<SORT_ROUNDS><<<(unsigned)nb, SORT_THREADS, lds, s>>>(ids, n, E, align, rows, hist, counts, offsets,
                                                                    perm, pos);
   return launched();
 }
 
-int moe_permute(int dtype, const void* x, int64_t ldx, const int32_t* perm, const int32_t* pos, int T, int k,
-                int64_t rows, int cols, void* out, int64_t ldo, void* stream) {
+int moe_permute(int dtype, const void* x, int64_t ldx, const int32_t* perm, const int32_t* pos, int64_t T,
+                int64_t k, int64_t rows, int64_t cols, void* out, int64_t ldo, void* stream) {
   int rc = check_rows(T, k, rows, cols);
   if (rc) return rc;
   const int b = elem_bytes(dtype);
@@ -634,8 +639,8 @@ int moe_permute(int dtype, const void* x, int64_t ldx, const int32_t* perm, cons
 }
 
 int moe_unpermute(int ytype, const void* y, int64_t ldy, int64_t rows, const int32_t* pos, const float* w,
-                  const float* base, int64_t ldb, int T, int k, int cols, int otype, void* out, int64_t ldo,
-                  void* stream) {
+                  const float* base, int64_t ldb, int64_t T, int64_t k, int64_t cols, int otype, void* out,
+                  int64_t ldo, void* stream) {
   int rc = check_rows(T, k, rows, cols);
   if (rc) return rc;
   const int by = elem_bytes(ytype), bo = elem_bytes(otype);
@@ -670,8 +675,8 @@ int moe_unpermute(int ytype, const void* y, int64_t ldy, int64_t rows, const int
 }
 
 int moe_unpermute_backward(int otype, const void* dout, int64_t ldd, int ytype, const void* y, int64_t ldy,
-                           const int32_t* perm, int64_t rows, const int32_t* pos, const float* w, int T, int k,
-                           int cols, void* dy, int64_t lddy, float* dw, void* stream) {
+                           const int32_t* perm, int64_t rows, const int32_t* pos, const float* w, int64_t T,
+                           int64_t k, int64_t cols, void* dy, int64_t lddy, float* dw, void* stream) {
   int rc = check_rows(T, k, rows, cols);
   if (rc) return rc;
   const int by = elem_bytes(ytype), bo = elem_bytes(otype);
@@ -703,10 +708,11 @@ int moe_unpermute_backward(int otype, const void* dout, int64_t ldd, int ytype, 
   });
 }
 
-int moe_gate_backward(const int32_t* ids, const float* w, const float* dw, int T, int k, int E, float* dz, int64_t ldz,
-                      void* stream) {
+int moe_gate_backward(const int32_t* ids, const float* w, const float* dw, int64_t T, int64_t k, int64_t E, float* dz,
+                      int64_t ldz, void* stream) {
   int rc = check_rows(T, k, 0, 1);
   if (rc) return rc;
+  if (E > I32_MAX) return bad(MOE_E_UNSUPPORTED, "more than 2^31 - 1 experts");
   if (E < 1 || ldz < E) return bad(MOE_E_INVAL, "need E >= 1 and a row stride of at least E");
   if (T == 0) return MOE_OK;
   if (!ids || !w || !dw || !dz) return bad(MOE_E_INVAL, "null argument");

@@ -483,9 +483,9 @@ void choose_form(const W4Args& a, bool gated, int otype, hipStream_t s) {
 }  // namespace
 
 extern "C" int moe_w4_matmul(int xtype, const void* x, int64_t ldx, int64_t x_rows, const int32_t* row_map,
-                             int map_div, const int32_t* offsets, const int32_t* counts, int E, int64_t rows,
-                             const uint8_t* codes, int stype, const void* scales, const void* zeros, int N, int K,
-                             int group, int gated, int otype, void* out, int64_t ldo, void* stream) {
+                             int64_t map_div, const int32_t* offsets, const int32_t* counts, int64_t E, int64_t rows,
+                             const uint8_t* codes, int stype, const void* scales, const void* zeros, int64_t N,
+                             int64_t K, int64_t group, int gated, int otype, void* out, int64_t ldo, void* stream) {
   if (xtype != MOE_T_BF16 && xtype != MOE_T_F16) return bad(MOE_E_INVAL, "x is bf16 or fp16");
   if (stype != MOE_T_BF16 && stype != MOE_T_F16) return bad(MOE_E_INVAL, "scales are bf16 or fp16");
   if (otype != xtype && otype != MOE_T_F32) return bad(MOE_E_INVAL, "out has x's type or is fp32");
@@ -496,19 +496,20 @@ extern "C" int moe_w4_matmul(int xtype, const void* x, int64_t ldx, int64_t x_ro
   if (K > MAX_K) return bad(MOE_E_UNSUPPORTED, "K over 32768");
   if (rows < 0 || rows > 0x7fffffffLL || x_rows < 0) return bad(MOE_E_INVAL, "rows outside [0, 2^31)");
   if (E < 1 || E > 1024) return bad(MOE_E_INVAL, "need 1 <= E <= 1024");
-  if ((int64_t)N * (K / group) > (1 << 30)) return bad(MOE_E_UNSUPPORTED, "more than 2^30 groups in a matrix");
-  if (K != group && (int64_t)E * N * (K / group) < 4) return bad(MOE_E_UNSUPPORTED, "fewer than 4 groups in all");
+  if (N > 1 << 30 || N * (K / group) > 1 << 30) return bad(MOE_E_UNSUPPORTED, "more than 2^30 groups in a matrix");
+  if (K != group && E * N * (K / group) < 4) return bad(MOE_E_UNSUPPORTED, "fewer than 4 groups in all");
   if (!offsets && (E != 1 || counts)) return bad(MOE_E_INVAL, "without offsets: one matrix and no counts");
-  if (row_map && map_div < 1) return bad(MOE_E_INVAL, "need map_div >= 1");
+  if (row_map && (map_div < 1 || map_div > 0x7fffffff)) return bad(MOE_E_INVAL, "need 1 <= map_div < 2^31");
   if (!row_map && x_rows < rows) return bad(MOE_E_INVAL, "x has fewer rows than out");
   if (ldx < K || ldx % 8) return bad(MOE_E_INVAL, "x's row stride: at least K and a multiple of 8");
   if (ldo < (gated ? N / 2 : N)) return bad(MOE_E_INVAL, "out's row stride smaller than its width");
   if (rows == 0) return MOE_OK;
   if ((x_rows && !x) || !codes || !scales || !out) return bad(MOE_E_INVAL, "null argument");
   if (((uintptr_t)x | (uintptr_t)codes) % 16) return bad(MOE_E_INVAL, "x and codes start on 16 bytes");
-  W4Args a{(const uint16_t*)x, ldx, x_rows, row_map, map_div, offsets, counts, E, rows, codes, (const uint16_t*)scales,
-           (const uint16_t*)zeros, N, K, K / group, 0, out, ldo};
-  const uint32_t runs = group < 128 ? 1 : group / 128;      // a step never passes a group of more than 128
+  // sizes came in 64 bits, so that none is cut before its check; they fit an int now
+  W4Args a{(const uint16_t*)x, ldx, x_rows, row_map, (int)map_div, offsets, counts, (int)E, rows, codes,
+           (const uint16_t*)scales, (const uint16_t*)zeros, (int)N, (int)K, (int)(K / group), 0, out, ldo};
+  const uint32_t runs = group < 128 ? 1 : (uint32_t)group / 128;      // a step never passes a group of more than 128
   a.per_group = ((1u << 31) + runs - 1) / runs;
   const hipStream_t s = (hipStream_t)stream;
   constexpr int BF = MOE_T_BF16, HF = MOE_T_F16;

@@ -32,13 +32,15 @@ _lib = B.lib
 
 def sort_rows(T: int, k: int, E: int, align: int = 1) -> int:
     """Rows perm (and the grouped tensors) need for any routing of T tokens."""
-    n = B.moe_sort_rows(T, k, E, align)
+    n = -1 if (T | k | E | align) >> 31 else B.moe_sort_rows(T, k, E, align)
     if n < 0:
-        raise ValueError("need T >= 0 and k, E, align >= 1")
+        raise ValueError("need T >= 0 and k, E, align >= 1, all below 2^31")
     return n
 
 
 def sort_workspace_bytes(T: int, k: int, E: int) -> int:
+    if (T | k | E) >> 31:
+        raise ValueError("need T >= 0 and k, E >= 1, all below 2^31")
     return B.moe_sort_workspace_bytes(T, k, E)
 
 
@@ -49,6 +51,8 @@ def sort(ids, counts, offsets, perm, pos, align=1, ws=None, stream=None):
     shape = ids.shape
     if len(shape) != 2:
         raise ValueError(f"ids: shape {tuple(shape)}, expected [T, k]")
+    if align >> 31:
+        raise ValueError(f"align: {align}, need 1 <= align < 2^31")
     T, k = shape
     dev, E, rows = ids.get_device(), counts.numel(), perm.numel()
     args = (A.whole("ids", ids, dev, _I32, shape), T, k, E, align, A.whole("counts", counts, dev, _I32, (E,)),

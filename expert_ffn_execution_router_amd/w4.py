@@ -56,6 +56,8 @@ def experts(x, offsets, out, codes, scales, zeros=None, counts=None, row_map=Non
     Rows in no segment stay as they were."""
     if codes.dim() != 3:
         raise ValueError(f"codes: shape {tuple(codes.shape)}, expected [E, N, K/2]")
+    if map_div >> 31:
+        raise ValueError(f"map_div: {map_div}, need 1 <= map_div < 2^31")
     dev, E, n = x.get_device(), codes.shape[0], out.shape[0]
     op = A.whole("offsets", offsets, dev, _I32, (E + 1,))
     cp = None if counts is None else A.whole("counts", counts, dev, _I32, (E,))

@@ -462,9 +462,10 @@ int moe_profile_end(moe_ctx* ctx, moe_profile* out);
  * Operators of their own: expert dispatch with its gradients, and products
  * with 4-bit weights.  No context; every pointer is device memory; sizes,
  * types and strides are checked on the host before any device work (message
- * in moe_last_error(NULL)).  Rows have a stride (ld*, in elements, at least
- * the width) and contiguous values.  No output shares memory with an input,
- * but for moe_unpermute's base.  Calls only enqueue kernels on stream, so
+ * in moe_last_error(NULL)); sizes are taken in 64 bits, so that none is cut to
+ * one that passes.  Rows have a stride (ld*, in elements, at least the width)
+ * and contiguous values.  No output shares memory with an input, but for
+ * moe_unpermute's base.  Calls only enqueue kernels on stream, so
  * they can be captured, and they keep nothing between calls: calls on
  * different streams are independent as long as their outputs and workspaces
  * are.  Equal inputs give equal bits.  T = 0 and rows = 0 are valid.
@@ -480,13 +481,14 @@ int moe_profile_end(moe_ctx* ctx, moe_profile* out);
  *                         -2 in the rows behind offsets[E]
  *   pos     int32 [T, k]  grouped row of a pair, -1 if dropped
  * Pairs of one expert keep their order.  rows: the length of perm, at least
- * moe_sort_rows (T*k + min(E, T*k)*(align-1), every routing fits).  ws:
+ * moe_sort_rows (T*k + min(E, T*k)*(align-1), every routing fits; -1 where an
+ * argument is out of range, 2^31 or more included).  ws:
  * moe_sort_workspace_bytes bytes (0 for at most 2048 pairs: ws may be NULL).
  * E <= 1024, k <= 64, T*k < 2^31.  INVAL, UNSUPPORTED, HIP. */
-int64_t moe_sort_rows(int T, int k, int E, int align);
-size_t moe_sort_workspace_bytes(int T, int k, int E);
-int moe_sort(const int32_t* ids, int T, int k, int E, int align, int32_t* counts, int32_t* offsets, int32_t* perm,
-             int64_t rows, int32_t* pos, void* ws, size_t ws_bytes, void* stream);
+int64_t moe_sort_rows(int64_t T, int64_t k, int64_t E, int64_t align);
+size_t moe_sort_workspace_bytes(int64_t T, int64_t k, int64_t E);
+int moe_sort(const int32_t* ids, int64_t T, int64_t k, int64_t E, int64_t align, int32_t* counts, int32_t* offsets,
+             int32_t* perm, int64_t rows, int32_t* pos, void* ws, size_t ws_bytes, void* stream);
 
 /* Token rows to their grouped places: out[pos[t,j]] = x[t], for each pair
  * with 0 <= pos < rows.  x [T, cols], out [rows, cols] of one MOE_T_* type.
@@ -494,8 +496,8 @@ int moe_sort(const int32_t* ids, int T, int k, int E, int align, int32_t* counts
  * behind the last segment are left as they were.  pos as moe_sort gives it: no
  * row twice, here and in moe_unpermute_backward, which store by it.  The
  * gradient of this call is moe_unpermute without weights. */
-int moe_permute(int dtype, const void* x, int64_t ldx, const int32_t* perm, const int32_t* pos, int T, int k,
-                int64_t rows, int cols, void* out, int64_t ldo, void* stream);
+int moe_permute(int dtype, const void* x, int64_t ldx, const int32_t* perm, const int32_t* pos, int64_t T,
+                int64_t k, int64_t rows, int64_t cols, void* out, int64_t ldo, void* stream);
 
 /* Grouped rows back to tokens: out[t] = base[t] + sum_j w[t,j] y[pos[t,j]]
  * over the pairs with 0 <= pos < rows, fp32 sums in choice order on top of
@@ -504,8 +506,8 @@ int moe_permute(int dtype, const void* x, int64_t ldx, const int32_t* perm, cons
  * it may be out itself, of the same stride, when out is fp32).  A token whose
  * pairs are all dropped gets base.  Types: equal, or one of y and out fp32. */
 int moe_unpermute(int ytype, const void* y, int64_t ldy, int64_t rows, const int32_t* pos, const float* w,
-                  const float* base, int64_t ldb, int T, int k, int cols, int otype, void* out, int64_t ldo,
-                  void* stream);
+                  const float* base, int64_t ldb, int64_t T, int64_t k, int64_t cols, int otype, void* out,
+                  int64_t ldo, void* stream);
 
 /* Gradients of moe_unpermute: dy[pos[t,j]] = w[t,j] dout[t] (type of y,
  * rounded once) and dw[t,j] = <dout[t], y[pos[t,j]]> (fp32 [T, k]; 0 for a
@@ -513,16 +515,16 @@ int moe_unpermute(int ytype, const void* y, int64_t ldy, int64_t rows, const int
  * dy's padding rows are set to zero, rows behind the last segment left as
  * they were.  dout has out's type (otype), dy y's; dy must not be y. */
 int moe_unpermute_backward(int otype, const void* dout, int64_t ldd, int ytype, const void* y, int64_t ldy,
-                           const int32_t* perm, int64_t rows, const int32_t* pos, const float* w, int T, int k,
-                           int cols, void* dy, int64_t lddy, float* dw, void* stream);
+                           const int32_t* perm, int64_t rows, const int32_t* pos, const float* w, int64_t T,
+                           int64_t k, int64_t cols, void* dy, int64_t lddy, float* dw, void* stream);
 
 /* Gradient of the gate: w = softmax over the k chosen logits (moe_route), so
  * dz[t,e] = sum over j with ids[t,j] = e of w_j (dw_j - sum_i w_i dw_i), and
  * 0 for experts that were not chosen.  ids int32, w and dw fp32 [T, k]; dz
  * fp32 [T, E] with row stride ldz, written whole.  ids outside [0, E) take
  * part in the inner sum only. */
-int moe_gate_backward(const int32_t* ids, const float* w, const float* dw, int T, int k, int E, float* dz, int64_t ldz,
-                      void* stream);
+int moe_gate_backward(const int32_t* ids, const float* w, const float* dw, int64_t T, int64_t k, int64_t E, float* dz,
+                      int64_t ldz, void* stream);
 
 /* Few rows times 4-bit weights with group scales:
  *   z[r,n] = sum_k x[r,k] (q[n,k] - zero[n,k/group]) scale[n,k/group]
@@ -545,10 +547,10 @@ int moe_gate_backward(const int32_t* ids, const float* w, const float* dw, int T
  * Any number of rows is valid; the design point is up to 64 per matrix.
  * E <= 1024, K <= 32768, N * K / group <= 2^30, at least 4 groups in all
  * unless group = K.  INVAL, UNSUPPORTED, HIP. */
-int moe_w4_matmul(int xtype, const void* x, int64_t ldx, int64_t x_rows, const int32_t* row_map, int map_div,
-                  const int32_t* offsets, const int32_t* counts, int E, int64_t rows, const uint8_t* codes, int stype,
-                  const void* scales, const void* zeros, int N, int K, int group, int gated, int otype, void* out,
-                  int64_t ldo, void* stream);
+int moe_w4_matmul(int xtype, const void* x, int64_t ldx, int64_t x_rows, const int32_t* row_map, int64_t map_div,
+                  const int32_t* offsets, const int32_t* counts, int64_t E, int64_t rows, const uint8_t* codes,
+                  int stype, const void* scales, const void* zeros, int64_t N, int64_t K, int64_t group, int gated,
+                  int otype, void* out, int64_t ldo, void* stream);
 
 #ifdef __cplusplus
 }
