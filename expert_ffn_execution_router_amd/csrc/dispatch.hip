@@ -14,6 +14,7 @@
 #include "fwd_ws.h"
 #include "moe.h"
 #include "route_dev.h"
+#include "spans.h"
 
 namespace {
 
@@ -504,6 +505,8 @@ int launched() {
   return e == hipSuccess ? MOE_OK : bad(MOE_E_HIP, hipGetErrorString(e));
 }
 
+int shared() { return bad(MOE_E_INVAL, "an output shares memory with an input or another output"); }
+
 int elem_bytes(int dt) { return dt == MOE_T_F32 ? 4 : (dt == MOE_T_BF16 || dt == MOE_T_F16 ? 2 : 0); }
 
 // Threads per row for `units` units, and the workgroups for T rows.
@@ -587,6 +590,10 @@ int moe_sort(const int32_t* ids, int64_t T, int64_t k, int64_t E, int64_t align,
   if (!counts || !offsets || (n && (!ids || !pos)) || (rows && !perm)) return bad(MOE_E_INVAL, "null argument");
   const size_t need = moe_sort_workspace_bytes(T, k, E);
   if (need && (!ws || ws_bytes < need)) return bad(MOE_E_INVAL, "workspace smaller than moe_sort_workspace_bytes");
+  if (outputs_shared({span(counts, E * 4), span(offsets, (E + 1) * 4), span(perm, rows * 4), span(pos, n * 4),
+                      span(ws, (int64_t)need)},
+                     {span(ids, n * 4)}))
+    return shared();
   const hipStream_t s = (hipStream_t)stream;
   const size_t lds = (size_t)((SORT_WAVES + 2) * E + SORT_WAVES) * 4;
   const long nb = sort_blocks(n);
@@ -622,6 +629,9 @@ int moe_permute(int dtype, const void* x, int64_t ldx, const int32_t* perm, cons
   const RowMap m = row_map_for((cols + V - 1) / V, T, &blocks);
   if (blocks + pads > MAX_BLOCKS) return bad(MOE_E_UNSUPPORTED, "too many rows");
   if (blocks + pads == 0) return MOE_OK;
+  if (outputs_shared({row_span(out, rows, cols, ldo, b)},
+                     {row_span(x, T, cols, ldx, b), span(perm, rows * 4), span(pos, T * k * 4)}))
+    return shared();
 #define GO(U, V, W)                                                                                               \
   permute_kernel<U, V, W><<<(unsigned)(blocks + pads), 256, 0, s>>>((const U*)x, ldx, pos, T, k, perm, rows, cols, \
                                                                     (unsigned)blocks, m, (U*)out, ldo)
@@ -653,10 +663,14 @@ int moe_unpermute(int ytype, const void* y, int64_t ldy, int64_t rows, const int
   const hipStream_t s = (hipStream_t)stream;
   // in place a value may not be read and written twice
   const bool single = base == out && cols % 8 != 0;
+  const bool clash = outputs_shared({row_span(out, T, cols, ldo, bo)},
+                                    {row_span(y, rows, cols, ldy, by), span(pos, T * k * 4), span(w, T * k * 4),
+                                     row_span(base == out ? nullptr : base, T, cols, ldb, 4)});
   return by_types(ytype, otype, single, cols, k, [&](auto a, auto o, auto v, auto jb) {
     typedef typename Elem<a.value>::type TY;
     typedef typename Elem<o.value>::type TO;
     if (rows == 0) {
+      if (clash) return shared();
       base_only_kernel<o.value><<<(unsigned)(((long)T * cols + 255) / 256), 256, 0, s>>>(base, ldb, T, cols, (TO*)out,
                                                                                        ldo);
       return launched();
@@ -664,6 +678,7 @@ int moe_unpermute(int ytype, const void* y, int64_t ldy, int64_t rows, const int
     long blocks;
     const RowMap m = row_map_for((cols + v.value - 1) / v.value, T, &blocks);
     if (blocks > MAX_BLOCKS) return bad(MOE_E_UNSUPPORTED, "too many rows");
+    if (clash) return shared();
     if (m.tpr_log2 == 8 && v.value > 1)
       unpermute_kernel<a.value, o.value, v.value, jb.value, true><<<(unsigned)blocks, 256, 0, s>>>(
           (const TY*)y, ldy, rows, pos, w, base, ldb, T, k, cols, m, (TO*)out, ldo);
@@ -685,10 +700,14 @@ int moe_unpermute_backward(int otype, const void* dout, int64_t ldd, int ytype, 
   if (T == 0 && (rows == 0 || !perm)) return MOE_OK;
   if ((T && (!dout || !pos || !w || !dw)) || (rows && (!y || !dy))) return bad(MOE_E_INVAL, "null argument");
   const hipStream_t s = (hipStream_t)stream;
+  const bool clash = outputs_shared({row_span(dy, rows, cols, lddy, by), span(dw, T * k * 4)},
+                                    {row_span(dout, T, cols, ldd, bo), row_span(y, rows, cols, ldy, by),
+                                     span(perm, rows * 4), span(pos, T * k * 4), span(w, T * k * 4)});
   return by_types(ytype, otype, false, cols, k, [&](auto a, auto o, auto v, auto jb) {
     typedef typename Elem<a.value>::type TY;
     typedef typename Elem<o.value>::type TO;
     if (rows == 0) {
+      if (clash) return shared();
       zero_kernel<<<(unsigned)(((long)T * k + 255) / 256), 256, 0, s>>>(dw, (long)T * k);
       return launched();
     }
@@ -696,6 +715,7 @@ int moe_unpermute_backward(int otype, const void* dout, int64_t ldd, int ytype, 
     const RowMap m = row_map_for((cols + v.value - 1) / v.value, T, &blocks);
     const long pads = perm ? (rows + PAD_ROWS - 1) / PAD_ROWS : 0;
     if (blocks + pads > MAX_BLOCKS) return bad(MOE_E_UNSUPPORTED, "too many rows");
+    if (clash) return shared();
     if (m.tpr_log2 == 8 && v.value > 1)
       unpermute_bwd_kernel<a.value, o.value, v.value, jb.value, true><<<(unsigned)(blocks + pads), 256, 0, s>>>(
           (const TO*)dout, ldd, (const TY*)y, ldy, perm, rows, pos, w, T, k, cols, (unsigned)blocks, m, (TY*)dy, lddy,
@@ -717,6 +737,8 @@ int moe_gate_backward(const int32_t* ids, const float* w, const float* dw, int64
   if (T == 0) return MOE_OK;
   if (!ids || !w || !dw || !dz) return bad(MOE_E_INVAL, "null argument");
   if ((T + 3L) / 4 > MAX_BLOCKS) return bad(MOE_E_UNSUPPORTED, "too many tokens");
+  if (outputs_shared({row_span(dz, T, E, ldz, 4)}, {span(ids, T * k * 4), span(w, T * k * 4), span(dw, T * k * 4)}))
+    return shared();
   gate_bwd_kernel<<<(unsigned)((T + 3L) / 4), 256, 0, (hipStream_t)stream>>>(ids, w, dw, T, k, E, dz, ldz);
   return launched();
 }

@@ -20,6 +20,7 @@
 #include "fwd_ws.h"
 #include "moe.h"
 #include "route_dev.h"
+#include "spans.h"
 
 #include <algorithm>
 
@@ -506,6 +507,11 @@ extern "C" int moe_w4_matmul(int xtype, const void* x, int64_t ldx, int64_t x_ro
   if (rows == 0) return MOE_OK;
   if ((x_rows && !x) || !codes || !scales || !out) return bad(MOE_E_INVAL, "null argument");
   if (((uintptr_t)x | (uintptr_t)codes) % 16) return bad(MOE_E_INVAL, "x and codes start on 16 bytes");
+  const int64_t values = E * N * (K / group) * 2;
+  if (outputs_shared({row_span(out, rows, gated ? N / 2 : N, ldo, otype == MOE_T_F32 ? 4 : 2)},
+                     {row_span(x, x_rows, K, ldx, 2), span(row_map, rows * 4), span(offsets, (E + 1) * 4),
+                      span(counts, E * 4), span(codes, E * N * (K / 2)), span(scales, values), span(zeros, values)}))
+    return bad(MOE_E_INVAL, "out shares memory with an input");
   // sizes came in 64 bits, so that none is cut before its check; they fit an int now
   W4Args a{(const uint16_t*)x, ldx, x_rows, row_map, (int)map_div, offsets, counts, (int)E, rows, codes,
            (const uint16_t*)scales, (const uint16_t*)zeros, (int)N, (int)K, (int)(K / group), 0, out, ldo};

@@ -7,8 +7,8 @@ are what sort() writes (moe_sort in include/moe.h has their meaning).  Hidden
 rows are bf16, fp16 or fp32 [rows, cols] views with contiguous rows.  Calls
 enqueue on the current stream of the tensors' device (or `stream`, which the
 caller orders after the work that made the inputs) and can be captured.  The
-memory from a result's first to its last value must not meet an input's,
-except for unpermute's base in place.
+memory from a result's first to its last value must not meet an input's or
+another result's, except for unpermute's base in place.
 
 A forward and backward of the experts' surroundings:
 

@@ -464,8 +464,9 @@ int moe_profile_end(moe_ctx* ctx, moe_profile* out);
  * types and strides are checked on the host before any device work (message
  * in moe_last_error(NULL)); sizes are taken in 64 bits, so that none is cut to
  * one that passes.  Rows have a stride (ld*, in elements, at least the width)
- * and contiguous values.  No output shares memory with an input, but for
- * moe_unpermute's base.  Calls only enqueue kernels on stream, so
+ * and contiguous values.  An output that shares memory with an input, but for
+ * moe_unpermute's base, or with another output is refused (rows of one stride
+ * may interleave, as column ranges of one buffer do).  Calls only enqueue kernels on stream, so
  * they can be captured, and they keep nothing between calls: calls on
  * different streams are independent as long as their outputs and workspaces
  * are.  Equal inputs give equal bits.  T = 0 and rows = 0 are valid.

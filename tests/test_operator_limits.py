@@ -89,3 +89,71 @@ def test_torch_layer_sizes_are_not_cut(B, over):
         w4.experts(torch.zeros(4, 64, **bf), torch.zeros(2, **i32), torch.zeros(4, 16, **bf),
                    torch.zeros(1, 16, 32, dtype=torch.uint8), torch.zeros(1, 16, 2, **bf),
                    row_map=torch.zeros(4, **i32), map_div=over)
+
+
+# addresses a megabyte apart: arrays of these calls that start there are apart
+A = [(i + 1) << 20 for i in range(8)]
+
+
+def check_shared(B, call, outputs, inputs, sizes):
+    """call refuses each output that begins at, or one byte before the end
+    of, an input or another output; sizes: bytes of each."""
+    for o in outputs:
+        for other in inputs + outputs:
+            if other == o:
+                continue
+            at = call.__kwdefaults__[other]
+            for p in (at, at + sizes[other] - 1, at - sizes[o] + 1):
+                assert call(**{o: p}) == B.MOE_E_INVAL, (o, other, p)
+                assert "shares memory" in B.last_error(), (o, other, p)
+
+
+def test_shared_memory_is_refused(B):
+    """A written tensor that meets a read one would be read half old, half
+    new; one that meets another written one would hold neither."""
+    def sort(*, ids=A[0], counts=A[1], offsets=A[2], perm=A[3], pos=A[4], ws=A[5]):
+        return B.moe_sort(ids, 1500, 2, 8, 1, counts, offsets, perm, 3000, pos, ws, 4096, None)
+    need = B.moe_sort_workspace_bytes(1500, 2, 8)
+    check_shared(B, sort, ["counts", "offsets", "perm", "pos"], ["ids", "ws"],
+                 dict(ids=12000, counts=32, offsets=36, perm=12000, pos=12000, ws=need))
+
+    def permute(*, x=A[0], perm=A[1], pos=A[2], out=A[3]):
+        return B.moe_permute(0, x, 64, perm, pos, 4, 2, 8, 64, out, 64, None)
+    check_shared(B, permute, ["out"], ["x", "perm", "pos"], dict(x=512, perm=32, pos=32, out=1024))
+
+    def unpermute(*, y=A[0], pos=A[1], w=A[2], base=A[3], out=A[4]):
+        return B.moe_unpermute(0, y, 64, 8, pos, w, base, 64, 4, 2, 64, 0, out, 64, None)
+    check_shared(B, unpermute, ["out"], ["y", "pos", "w"], dict(y=1024, pos=32, w=32, base=1024, out=512))
+    assert unpermute(out=A[3] + 2) == unpermute(out=A[3] - 2) == B.MOE_E_INVAL
+
+    def no_rows(*, base=A[3], out=A[4]):
+        return B.moe_unpermute(2, None, 64, 0, A[0], None, base, 64, 4, 2, 64, 2, out, 64, None)
+    assert no_rows(out=A[3] + 4) == no_rows(base=A[4] + 4) == B.MOE_E_INVAL
+
+    def backward(*, dout=A[0], y=A[1], perm=A[2], pos=A[3], w=A[4], dy=A[5], dw=A[6]):
+        return B.moe_unpermute_backward(0, dout, 64, 0, y, 64, perm, 8, pos, w, 4, 2, 64, dy, 64, dw, None)
+    check_shared(B, backward, ["dy", "dw"], ["dout", "y", "perm", "pos", "w"],
+                 dict(dout=512, y=1024, perm=32, pos=32, w=32, dy=1024, dw=32))
+
+    def gate(*, ids=A[0], w=A[1], dw=A[2], dz=A[3]):
+        return B.moe_gate_backward(ids, w, dw, 4, 2, 8, dz, 8, None)
+    check_shared(B, gate, ["dz"], ["ids", "w", "dw"], dict(ids=32, w=32, dw=32, dz=128))
+
+    def mm(*, x=A[0], row_map=A[1], offsets=A[2], counts=A[3], codes=A[4], scales=A[5], zeros=A[6], out=A[7]):
+        return B.moe_w4_matmul(0, x, 256, 4, row_map, 1, offsets, counts, 2, 4, codes, 0, scales, zeros, 32, 256, 128,
+                               0, 0, out, 32, None)
+    check_shared(B, mm, ["out"], ["x", "row_map", "offsets", "counts", "codes", "scales", "zeros"],
+                 dict(x=2048, row_map=16, offsets=12, counts=8, codes=8192, scales=256, zeros=256, out=256))
+
+
+def test_rows_that_cross_are_refused(B):
+    """Rows of one buffer: columns that meet, and rows of different strides."""
+    def permute(x, ldx, out, ldo, rows=8):
+        return B.moe_permute(0, x, ldx, None, A[6], 4, 2, rows, 64, out, ldo, None)
+    base = A[0]
+    assert permute(base, 256, base + 2 * 63, 256) == B.MOE_E_INVAL         # the last column
+    assert permute(base, 256, base + 2 * (256 - 63), 256) == B.MOE_E_INVAL  # the first column of the next row
+    assert permute(base + 2 * 63, 256, base, 256) == B.MOE_E_INVAL
+    assert permute(base, 256, base + 128, 264) == B.MOE_E_INVAL            # other strides: whole ranges
+    assert permute(base, 2 ** 60, base + 2 ** 62, 64) == B.MOE_E_INVAL     # no wrap in 64 bits
+    assert permute(base, 256, base + 2 * 63, 64, rows=1) == B.MOE_E_INVAL  # one row, across two
