@@ -590,6 +590,7 @@ int moe_sort(const int32_t* ids, int64_t T, int64_t k, int64_t E, int64_t align,
   if (!counts || !offsets || (n && (!ids || !pos)) || (rows && !perm)) return bad(MOE_E_INVAL, "null argument");
   const size_t need = moe_sort_workspace_bytes(T, k, E);
   if (need && (!ws || ws_bytes < need)) return bad(MOE_E_INVAL, "workspace smaller than moe_sort_workspace_bytes");
+  if (need && (uintptr_t)ws % 4) return bad(MOE_E_INVAL, "the workspace holds ints: it starts on 4 bytes");
   if (outputs_shared({span(counts, E * 4), span(offsets, (E + 1) * 4), span(perm, rows * 4), span(pos, n * 4),
                       span(ws, (int64_t)need)},
                      {span(ids, n * 4)}))

@@ -46,8 +46,8 @@ def sort_workspace_bytes(T: int, k: int, E: int) -> int:
 
 def sort(ids, counts, offsets, perm, pos, align=1, ws=None, stream=None):
     """Groups the pairs of ids by expert, segments padded to multiples of
-    align.  ws: uint8 tensor of sort_workspace_bytes; None allocates one where
-    it is needed (more than 2048 pairs)."""
+    align.  ws: uint8 tensor of sort_workspace_bytes that starts on 4 bytes;
+    None allocates one where it is needed (more than 2048 pairs)."""
     shape = ids.shape
     if len(shape) != 2:
         raise ValueError(f"ids: shape {tuple(shape)}, expected [T, k]")

@@ -484,7 +484,8 @@ int moe_profile_end(moe_ctx* ctx, moe_profile* out);
  * Pairs of one expert keep their order.  rows: the length of perm, at least
  * moe_sort_rows (T*k + min(E, T*k)*(align-1), every routing fits; -1 where an
  * argument is out of range, 2^31 or more included).  ws:
- * moe_sort_workspace_bytes bytes (0 for at most 2048 pairs: ws may be NULL).
+ * moe_sort_workspace_bytes bytes on 4 (0 for at most 2048 pairs: ws may be
+ * NULL).
  * E <= 1024, k <= 64, T*k < 2^31.  INVAL, UNSUPPORTED, HIP. */
 int64_t moe_sort_rows(int64_t T, int64_t k, int64_t E, int64_t align);
 size_t moe_sort_workspace_bytes(int64_t T, int64_t k, int64_t E);

@@ -157,3 +157,12 @@ def test_rows_that_cross_are_refused(B):
     assert permute(base, 256, base + 128, 264) == B.MOE_E_INVAL            # other strides: whole ranges
     assert permute(base, 2 ** 60, base + 2 ** 62, 64) == B.MOE_E_INVAL     # no wrap in 64 bits
     assert permute(base, 256, base + 2 * 63, 64, rows=1) == B.MOE_E_INVAL  # one row, across two
+
+
+def test_workspace_off_its_alignment_is_refused(B):
+    """The workspace is any bytes to the caller and ints to the kernels."""
+    def sort(T, ws):
+        return B.moe_sort(A[0], T, 2, 8, 1, A[1], A[2], A[3], 3000, A[4], ws, 4096, None)
+    for off in (1, 2, 3):
+        assert sort(1500, A[5] + off) == B.MOE_E_INVAL
+        assert "4 bytes" in B.last_error()
