@@ -15,6 +15,12 @@ BYTES = {B.MOE_T_BF16: 2, B.MOE_T_F16: 2, B.MOE_T_F32: 4}
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
+_grad_enabled = torch.is_grad_enabled
+
+
+def _no_graph(name):
+    raise ValueError(f"{name}: requires grad, and the call records no graph: call it under torch.no_grad(), or in the "
+                     "forward and backward of a torch.autograd.Function")
 
 
 def rows(name, t, dev, n, cols, types=TYPES):
@@ -28,6 +34,8 @@ def rows(name, t, dev, n, cols, types=TYPES):
         raise ValueError(f"{name}: shape {tuple(shape)}, expected [{'rows' if n is None else n}, {cols}]")
     if t.get_device() != dev:
         raise ValueError(f"{name}: on {t.device}, expected device {dev}")
+    if t.requires_grad and _grad_enabled():
+        _no_graph(name)
     p, m = t.data_ptr(), shape[0]
     if m == 0:
         return code, p, cols, p
@@ -47,6 +55,8 @@ def whole(name, t, dev, dtype, shape):
         raise ValueError(f"{name}: on {t.device}, expected device {dev}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: has to be contiguous")
+    if t.requires_grad and _grad_enabled():
+        _no_graph(name)
     return t.data_ptr()
 
 

@@ -8,7 +8,8 @@ rows are bf16, fp16 or fp32 [rows, cols] views with contiguous rows.  Calls
 enqueue on the current stream of the tensors' device (or `stream`, which the
 caller orders after the work that made the inputs) and can be captured.  The
 memory from a result's first to its last value must not meet an input's or
-another result's, except for unpermute's base in place.
+another result's, except for unpermute's base in place.  No call records a
+graph: with gradients enabled, a tensor that requires grad is refused.
 
 A forward and backward of the experts' surroundings:
 

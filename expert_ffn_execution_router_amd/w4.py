@@ -7,7 +7,9 @@ zeros: the same shape in x's type, or None for 8.  group: 32, 64 or a
 multiple of 128.  x: bf16 or fp16, out: x's type or fp32.  gated: the matrix
 is [gate; up] stacked and out = silu(x gate^T) * (x up^T).
 
-The memory from out's first to its last value must not meet an input's.
+The memory from out's first to its last value must not meet an input's.  No
+call records a graph: with gradients enabled, a tensor that requires grad is
+refused.
 moe_w4_matmul in include/moe.h has the details; calls enqueue on the current
 stream of the tensors' device (or `stream`) and can be captured.
 """

@@ -161,8 +161,43 @@ def test_rows_that_cross_are_refused(B):
 
 def test_workspace_off_its_alignment_is_refused(B):
     """The workspace is any bytes to the caller and ints to the kernels."""
-    def sort(T, ws):
-        return B.moe_sort(A[0], T, 2, 8, 1, A[1], A[2], A[3], 3000, A[4], ws, 4096, None)
     for off in (1, 2, 3):
-        assert sort(1500, A[5] + off) == B.MOE_E_INVAL
+        assert B.moe_sort(A[0], 1500, 2, 8, 1, A[1], A[2], A[3], 3000, A[4], A[5] + off, 4096, None) == B.MOE_E_INVAL
         assert "4 bytes" in B.last_error()
+
+
+def test_tensors_that_want_a_graph_are_refused(B):
+    """Results are written past autograd, so a tensor that requires grad would
+    lose its gradient without a word; without gradients it is a plain tensor
+    (here refused last, for being on the CPU)."""
+    from expert_ffn_execution_router_amd import dispatch as D
+    from expert_ffn_execution_router_amd import w4
+    perm, pos, ids = (torch.zeros(s, dtype=torch.int32) for s in (8, (4, 2), (4, 2)))
+    bf = dict(dtype=torch.bfloat16)
+    t = dict(x=torch.zeros(4, 64, **bf), xs=torch.zeros(8, 64, **bf), w=torch.zeros(4, 2), base=torch.zeros(4, 64),
+             out=torch.zeros(4, 64, **bf), dy=torch.zeros(8, 64, **bf), dw=torch.zeros(4, 2), dz=torch.zeros(4, 8),
+             scales=torch.zeros(16, 2, **bf), zeros=torch.zeros(16, 2, **bf), z=torch.zeros(4, 16, **bf))
+    codes, eo = torch.zeros(16, 32, dtype=torch.uint8), torch.zeros(2, dtype=torch.int32)
+    calls = [("x xs", lambda v: D.permute(v["x"], perm, pos, v["xs"])),
+             ("xs w out base", lambda v: D.unpermute(v["xs"], pos, v["w"], v["out"], base=v["base"])),
+             ("xs out", lambda v: D.permute_backward(v["xs"], pos, v["out"])),
+             ("out xs w dy dw", lambda v: D.unpermute_backward(v["out"], v["xs"], perm, pos, v["w"], v["dy"], v["dw"])),
+             ("w dw dz", lambda v: D.gate_backward(ids, v["w"], v["dw"], v["dz"])),
+             ("x scales zeros z", lambda v: w4.linear(v["x"], v["z"], codes, v["scales"], zeros=v["zeros"])),
+             ("x scales zeros z", lambda v: w4.experts(v["x"], eo, v["z"], codes[None], v["scales"][None],
+                                                       zeros=v["zeros"][None]))]
+    for names, call in calls:
+        for n in names.split():
+            v = dict(t, **{n: t[n].clone().requires_grad_()})
+            with pytest.raises(ValueError, match="requires grad"):
+                call(v)
+            with torch.no_grad(), pytest.raises(ValueError, match="on the GPU"):
+                call(v)
+
+    class Copy(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            D.permute(x, perm, pos, t["xs"])
+
+    with pytest.raises(ValueError, match="on the GPU"):
+        Copy.apply(t["x"].clone().requires_grad_())
