@@ -498,7 +498,10 @@ extern "C" int moe_w4_matmul(int xtype, const void* x, int64_t ldx, int64_t x_ro
   if (rows < 0 || rows > 0x7fffffffLL || x_rows < 0) return bad(MOE_E_INVAL, "rows outside [0, 2^31)");
   if (E < 1 || E > 1024) return bad(MOE_E_INVAL, "need 1 <= E <= 1024");
   if (N > 1 << 30 || N * (K / group) > 1 << 30) return bad(MOE_E_UNSUPPORTED, "more than 2^30 groups in a matrix");
-  if (K != group && E * N * (K / group) < 4) return bad(MOE_E_UNSUPPORTED, "fewer than 4 groups in all");
+  // the group values of a step come in one load: 4 of them, 2 for groups of 64
+  // (K holds two such groups at least), 1 otherwise
+  if (group == 32 && K != group && E * N * (K / group) < 4)
+    return bad(MOE_E_UNSUPPORTED, "fewer than 4 groups of 32 in all");
   if (!offsets && (E != 1 || counts)) return bad(MOE_E_INVAL, "without offsets: one matrix and no counts");
   if (row_map && (map_div < 1 || map_div > 0x7fffffff)) return bad(MOE_E_INVAL, "need 1 <= map_div < 2^31");
   if (!row_map && x_rows < rows) return bad(MOE_E_INVAL, "x has fewer rows than out");

@@ -547,8 +547,8 @@ int moe_gate_backward(const int32_t* ids, const float* w, const float* dw, int64
  *     row_map[r] / map_div (moe_sort's perm with map_div = k reads token
  *     rows); a map entry outside x reads a row of zeros.
  * Any number of rows is valid; the design point is up to 64 per matrix.
- * E <= 1024, K <= 32768, N * K / group <= 2^30, at least 4 groups in all
- * unless group = K.  INVAL, UNSUPPORTED, HIP. */
+ * E <= 1024, K <= 32768, N * K / group <= 2^30, groups of 32 at least 4 in
+ * all unless K = 32.  INVAL, UNSUPPORTED, HIP. */
 int moe_w4_matmul(int xtype, const void* x, int64_t ldx, int64_t x_rows, const int32_t* row_map, int64_t map_div,
                   const int32_t* offsets, const int32_t* counts, int64_t E, int64_t rows, const uint8_t* codes,
                   int stype, const void* scales, const void* zeros, int64_t N, int64_t K, int64_t group, int gated,

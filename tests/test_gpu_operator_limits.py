@@ -6,11 +6,13 @@ import torch
 
 from expert_ffn_execution_router_amd import binding as B
 from expert_ffn_execution_router_amd import dispatch as D
+from expert_ffn_execution_router_amd import w4
 from oracle import dispatch as O
+from oracle import w4 as OW
 
 pytestmark = pytest.mark.gpu
 
-BF = torch.bfloat16
+BF, HF = torch.bfloat16, torch.float16
 
 
 def np64(t):
@@ -42,3 +44,43 @@ def test_neighbours_and_column_ranges_of_one_buffer():
     assert rc == 0
     assert np.array_equal(np64(out), O.permute(rows, ref[2], ref[3], want))
     assert np.array_equal(np64(x), rows)
+
+
+# E, N, K, group: as few group values as one load of a step reads, or fewer in
+# a matrix of several
+FEWEST = [(1, 1, 128, 32), (1, 2, 64, 32), (2, 1, 64, 32), (3, 1, 64, 32), (5, 1, 96, 32), (4, 1, 32, 32), (1, 1, 32, 32),
+          (1, 1, 128, 64), (1, 1, 192, 64), (3, 1, 128, 64), (1, 1, 256, 128), (1, 1, 384, 128), (2, 1, 256, 128),
+          (1, 1, 512, 256), (1, 1, 64, 64)]
+
+
+@pytest.mark.parametrize("xt", [BF, HF])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("E,N,K,group", FEWEST)
+def test_fewest_group_values(E, N, K, group, zeros, xt):
+    """Exact integers; what lies beside the scales and zeros is NaN, so a
+    value read from there would show, were its x a zero."""
+    print(f"fewest E={E} N={N} K={K} group={group} zeros={zeros} {xt}", flush=True)
+    rng = np.random.default_rng(E + N + K)
+    q = rng.integers(0, 16, (E, N, K))
+    s = 2.0 ** rng.integers(-3, 3, (E, N, K // group))
+    z = rng.integers(0, 16, s.shape).astype(np.float64) if zeros else None
+    xv = rng.integers(-4, 5, (2 * E + 1, K)).astype(np.float64)
+
+    def among_nan(v):
+        b = torch.full((v.size + 32,), float("nan"), dtype=xt, device="cuda")
+        b[16:16 + v.size] = torch.from_numpy(v.reshape(-1)).to(xt).cuda()
+        return b[16:16 + v.size].view(v.shape)
+    sd, zd = among_nan(s), among_nan(z) if zeros else None
+    x = torch.from_numpy(xv).to(xt).cuda()
+    out = torch.full((2 * E + 1, N), 5.0, device="cuda")
+    codes = torch.from_numpy(OW.pack(q)).cuda()
+    o = torch.arange(0, 2 * E + 1, 2, dtype=torch.int32, device="cuda")
+    w4.experts(x, o, out, codes, sd, zeros=zd)
+    for e in range(E):
+        ref, _ = OW.product(xv[2 * e:2 * e + 2], q[e], s[e], None if z is None else z[e], group)
+        assert np.array_equal(np64(out[2 * e:2 * e + 2]), ref), e
+    assert (out[2 * E] == 5.0).all()
+    if E == 1:
+        dense = torch.empty(2, N, device="cuda")
+        w4.linear(x[:2], dense, codes[0], sd[0], zeros=None if zd is None else zd[0])
+        assert torch.equal(dense, out[:2])

@@ -201,3 +201,14 @@ def test_tensors_that_want_a_graph_are_refused(B):
 
     with pytest.raises(ValueError, match="on the GPU"):
         Copy.apply(t["x"].clone().requires_grad_())
+
+
+def test_fewest_groups(B):
+    """Only groups of 32 are too few by themselves (no rows: nothing runs)."""
+    def mm(N, K, group, E=1):
+        return B.moe_w4_matmul(0, P, K, 4, None, 1, P if E > 1 else None, None, E, 0, P, 0, P, None, N, K, group, 0, 0,
+                               P, N, None)
+    for shape in ((1, 128, 64), (1, 192, 64), (1, 256, 128), (1, 384, 128), (1, 512, 256), (1, 128, 32), (2, 64, 32),
+                  (1, 32, 32), (1, 64, 32, 2)):
+        assert mm(*shape) == 0, shape
+    assert mm(1, 64, 32) == mm(1, 96, 32) == B.MOE_E_UNSUPPORTED
