@@ -5,7 +5,9 @@ codes: uint8 [N, K/2] (or [E, N, K/2], one matrix per expert), two codes per
 byte, even input in the low nibble.  scales: bf16 or fp16 [..., N, K/group];
 zeros: the same shape in x's type, or None for 8.  group: 32, 64 or a
 multiple of 128.  x: bf16 or fp16, out: x's type or fp32.  gated: the matrix
-is [gate; up] stacked and out = silu(x gate^T) * (x up^T).
+is [gate; up] stacked and out = silu(x gate^T) * (x up^T).  x is finite, in
+bf16 below 2^116 with zeros of up to 16 (fp32 holds |x| (q + |zero|) summed
+over 128 inputs; past it a row may be infinite or NaN where the result is not).
 
 The memory from out's first to its last value must not meet an input's.  No
 call records a graph: with gradients enabled, a tensor that requires grad is

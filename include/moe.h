@@ -538,7 +538,10 @@ int moe_gate_backward(const int32_t* ids, const float* w, const float* dw, int64
  * out[r] = silu(z[r, :N/2]) * z[r, N/2:], [rows, N/2]; else out [rows, N].
  * x bf16 or fp16 [x_rows, K], on 16 bytes, stride a multiple of 8, finite (a
  * row with an infinity or NaN gives NaN, other rows are not touched by it);
- * scales and zeros finite.
+ * scales and zeros finite.  q x and zero x are summed apart, up to 128 inputs
+ * together, before their difference is scaled: fp32 has to hold the sum of
+ * |x| (q + |zero|) over these.  It does for |x| < 2^116 (any fp16) with zeros
+ * of up to 16; past it a row may be infinite or NaN where z is not.
  *   dense (offsets NULL, E = 1): out row r from x row r.
  *   per expert: grouped rows offsets[e] .. + counts[e] (counts NULL: up to
  *     offsets[e+1]) use matrix e; offsets int32 [E+1], counts int32 [E] as

@@ -84,3 +84,26 @@ def test_fewest_group_values(E, N, K, group, zeros, xt):
         dense = torch.empty(2, N, device="cuda")
         w4.linear(x[:2], dense, codes[0], sd[0], zeros=None if zd is None else zd[0])
         assert torch.equal(dense, out[:2])
+
+
+@pytest.mark.parametrize("zero", [None, -16.0, 16.0])
+@pytest.mark.parametrize("K,group", [(256, 32), (256, 64), (640, 128), (1024, 512), (6144, 64), (6144, 2048)])
+def test_largest_inputs(K, group, zero):
+    """bf16 inputs just below 2^116, all of one sign in a row, against the
+    codes that make its sums largest.  x = 15 2^112: q x, zero x and all their
+    sums are integers times 2^112, below 31 15 K < 2^22 of them, so no sum
+    rounds; the scale is a power of two."""
+    print(f"largest K={K} group={group} zero={zero}", flush=True)
+    rng = np.random.default_rng(K)
+    q = rng.integers(0, 16, (20, K))
+    q[:8], q[8:12] = 15, 0
+    s = np.full((20, K // group), 2.0 ** -20)
+    z = None if zero is None else np.full(s.shape, zero)
+    xv = np.full((5, K), 15 * 2.0 ** 112) * np.array([1, -1, 1, -1, 1])[:, None]
+    xv[4, ::3] = 0
+    sd = torch.from_numpy(s).to(BF).cuda()
+    zd = None if zero is None else torch.from_numpy(z).to(BF).cuda()
+    out = torch.empty(5, 20, device="cuda")
+    w4.linear(torch.from_numpy(xv).to(BF).cuda(), out, torch.from_numpy(OW.pack(q)).cuda(), sd, zeros=zd)
+    ref, _ = OW.product(xv, q, s, z, group)
+    assert np.array_equal(np64(out), ref)
