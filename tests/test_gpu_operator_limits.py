@@ -107,3 +107,110 @@ def test_largest_inputs(K, group, zero):
     w4.linear(torch.from_numpy(xv).to(BF).cuda(), out, torch.from_numpy(OW.pack(q)).cuda(), sd, zeros=zd)
     ref, _ = OW.product(xv, q, s, z, group)
     assert np.array_equal(np64(out), ref)
+
+
+# ---------------------------------------------------------------------------
+# every path through the 4-bit kernel
+# ---------------------------------------------------------------------------
+# Integer x in [-2, 2], codes and zeros in [0, 15], scales 1/2 or 1: all sums
+# are integers and halves below 60 K < 2^19, so fp32 rounds none, in any order,
+# and a product equals the float64 one in every value.  A gated result takes
+# exp, sum, quotient and two products from exact z: 8 roundings of 2^-23, and
+# where exp overflows (gate below -88.7) |silu| < 3e-37 becomes 0.
+
+def integers(g, E, N, K, group, zeros, xt):
+    codes = torch.randint(0, 256, (E, N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = torch.randint(1, 3, (E, N, K // group), generator=g, device="cuda").to(xt) / 2
+    z = torch.randint(0, 16, s.shape, generator=g, device="cuda").to(xt) if zeros else None
+    return codes, s, z
+
+
+def product64(x, codes, s, z, group):
+    q = torch.stack([codes & 15, codes >> 4], -1).flatten(-2).double()
+    z = 8.0 if z is None else z.double().repeat_interleave(group, -1)
+    w = (q - z) * s.double().repeat_interleave(group, -1)
+    return x.double() @ w.t().contiguous()
+
+
+def same(out, z, gated):
+    if not gated:
+        assert torch.equal(out.double(), z)
+        return
+    n = z.shape[1] // 2
+    gate, up = z[:, :n], z[:, n:]
+    ref = gate / (1 + torch.exp(-gate)) * up
+    assert ((out.double() - ref).abs() <= 8 * 2.0 ** -23 * ref.abs() + 1e-36 * (1 + up.abs())).all()
+
+
+# tokens, choices, experts (0: dense rows), width of out, inputs.  The launch
+# gives each workgroup 2 to 8 tile groups (1 where a form without gate has half
+# as many), and where row blocks go in turn it has 170 places for 188 of them
+# (gated 87), or 341 (178) for a bound of 362 that the dropped pairs leave
+# unfilled.
+PATHS = {
+    "tile groups in turn": (64, 8, 128, 544, 1024),
+    "eight tile groups in turn, the last tile ragged": (64, 8, 128, 1000, 256),
+    "tile groups in turn, in passes": (640, 0, 0, 3300, 4224),
+    "grouped rows in passes": (64, 8, 128, 400, 2560),
+    "row blocks in turn": (3000, 0, 0, 6000, 640),
+    "row blocks in turn, in passes": (3000, 0, 0, 6000, 4224),
+    "row blocks in turn, fewer than their bound": (700, 4, 200, 2912, 256),
+    "four steps held, the last wave's mostly past the inputs": (1040, 0, 0, 2048, 2176),
+    "four steps held": (1040, 0, 0, 2048, 4096),
+    "four steps held, grouped rows": (64, 8, 128, 1000, 2176),
+}
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("kind", [32, 64, 128])
+@pytest.mark.parametrize("path", PATHS)
+def test_every_path_is_exact(path, kind, zeros, gated):
+    T, k, E, width, K = PATHS[path]
+    group = kind if kind < 128 else next(n for n in (1024, 512, 256, 128) if K % n == 0)
+    xt = HF if kind == 64 else BF
+    print(f"{path}: T={T} k={k} E={E} width={width} K={K} group={group} zeros={zeros} gated={gated} {xt}", flush=True)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T + K + kind)
+    codes, s, z = integers(g, max(E, 1), 2 * width if gated else width, K, group, zeros, xt)
+    x = torch.randint(-2, 3, (T, K), generator=g, device="cuda").to(xt)
+    if not E:
+        out = torch.full((T, width + 1), 5.0, device="cuda")
+        w4.linear(x, out[:, :width], codes[0], s[0], zeros=None if z is None else z[0], gated=gated)
+        same(out[:, :width], product64(x, codes[0], s[0], None if z is None else z[0], group), gated)
+        assert (out[:, width] == 5.0).all()
+        return
+    i32 = dict(dtype=torch.int32, device="cuda")
+    bias = -torch.log(torch.arange(1, E + 1, device="cuda"))       # a few experts take many rows
+    score = torch.rand(T, E, generator=g, device="cuda") * 4 + bias
+    ids = torch.topk(score, k, dim=1).indices.to(torch.int32)
+    ids[torch.rand(T, k, generator=g, device="cuda") < 0.2] = -1
+    counts, offsets, perm, pos = (torch.zeros(n, **i32) for n in (E, E + 1, T * k, (T, k)))
+    D.sort(ids, counts, offsets, perm, pos)
+    out = torch.full((T * k, width + 1), 5.0, device="cuda")
+    w4.experts(x, offsets, out[:, :width], codes, s, zeros=z, row_map=perm, map_div=k, gated=gated)
+    o = offsets.tolist()
+    assert max(b - a for a, b in zip(o, o[1:])) > 16
+    for e in range(E):
+        if o[e + 1] > o[e]:
+            rows = slice(o[e], o[e + 1])
+            xe = x[torch.div(perm[rows], k, rounding_mode="floor").long()]
+            same(out[rows, :width], product64(xe, codes[e], s[e], None if z is None else z[e], group), gated)
+    assert (out[o[E]:] == 5.0).all() and (out[:, width] == 5.0).all()
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("T,N,K,group", [(2, 48, 4096, 128), (19, 40, 6144, 32), (17, 34, 6144, 1024), (4, 20, 8320, 64),
+                                         (33, 33, 5120, 1024), (3, 50, 32768, 256)])
+def test_long_rows_are_exact(T, N, K, group, zeros):
+    """Rows that are taken in passes; K = 32768: sums below 60 K < 2^21, halves
+    of them still within 24 bits."""
+    print(f"long rows T={T} N={N} K={K} group={group} zeros={zeros}", flush=True)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(K)
+    for xt in (BF, HF):
+        codes, s, z = integers(g, 1, N, K, group, zeros, xt)
+        x = torch.randint(-2, 3, (T, K), generator=g, device="cuda").to(xt)
+        out = torch.empty(T, N, device="cuda")
+        w4.linear(x, out, codes[0], s[0], zeros=None if z is None else z[0])
+        same(out, product64(x, codes[0], s[0], None if z is None else z[0], group), False)
