@@ -13,6 +13,7 @@ TYPES = {torch.bfloat16: B.MOE_T_BF16, torch.float16: B.MOE_T_F16, torch.float32
 F32_ONLY = {torch.float32: B.MOE_T_F32}
 BYTES = {B.MOE_T_BF16: 2, B.MOE_T_F16: 2, B.MOE_T_F32: 4}
 
+_I32 = torch.int32
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 _grad_enabled = torch.is_grad_enabled
@@ -47,23 +48,22 @@ def rows(name, t, dev, n, cols, types=TYPES):
     return code, p, step, p + ((m - 1) * step + cols) * BYTES[code]
 
 
-def whole(name, t, dev, dtype, shape):
-    """Address of a contiguous tensor of one type and shape."""
-    if t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected {dtype} {tuple(shape)}")
+def whole(name, t, dev, dtype, shape=None):
+    """Address of a contiguous tensor of one type and shape (None: the caller
+    has looked at its shape)."""
+    if t.dtype != dtype or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected {dtype} {tuple(shape or t.shape)}")
     if t.get_device() != dev:
         raise ValueError(f"{name}: on {t.device}, expected device {dev}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: has to be contiguous")
-    if t.requires_grad and _grad_enabled():
+    if dtype is not _I32 and t.requires_grad and _grad_enabled():
         _no_graph(name)
     return t.data_ptr()
 
 
-def apart(name, p, end, q, qend):
-    """The written range [p, end) must not meet the read range [q, qend)."""
-    if q < end and p < qend:
-        raise ValueError(f"{name}: overlaps an input")
+def overlaps(name):
+    raise ValueError(f"{name}: overlaps an input")
 
 
 def launch(fn, dev, stream, *args):

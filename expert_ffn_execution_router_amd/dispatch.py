@@ -56,7 +56,7 @@ def sort(ids, counts, offsets, perm, pos, align=1, ws=None, stream=None):
         raise ValueError(f"align: {align}, need 1 <= align < 2^31")
     T, k = shape
     dev, E, rows = ids.get_device(), counts.numel(), perm.numel()
-    args = (A.whole("ids", ids, dev, _I32, shape), T, k, E, align, A.whole("counts", counts, dev, _I32, (E,)),
+    args = (A.whole("ids", ids, dev, _I32), T, k, E, align, A.whole("counts", counts, dev, _I32, (E,)),
             A.whole("offsets", offsets, dev, _I32, (E + 1,)), A.whole("perm", perm, dev, _I32, (rows,)), rows,
             A.whole("pos", pos, dev, _I32, shape))
     if ws is None:
@@ -67,7 +67,7 @@ def sort(ids, counts, offsets, perm, pos, align=1, ws=None, stream=None):
             else:
                 with torch.cuda.stream(stream):
                     ws = torch.empty(need, dtype=torch.uint8, device=ids.device)
-    wp, wn = (None, 0) if ws is None else (A.whole("ws", ws, dev, torch.uint8, (ws.numel(),)), ws.numel())
+    wp, wn = (None, 0) if ws is None else (A.whole("ws", ws, dev, torch.uint8), ws.numel())
     A.launch(_lib().moe_sort, dev, stream, *args, wp, wn)
 
 
@@ -75,7 +75,7 @@ def _tokens(name, pos, dev):
     shape = pos.shape
     if len(shape) != 2:
         raise ValueError(f"{name}: shape {tuple(shape)}, expected [T, k]")
-    return A.whole(name, pos, dev, _I32, shape), shape
+    return A.whole(name, pos, dev, _I32), shape
 
 
 def permute(x, perm, pos, out, stream=None):
@@ -87,7 +87,8 @@ def permute(x, perm, pos, out, stream=None):
     ot, op, ldo, oe = A.rows("out", out, dev, n, cols)
     if ot != dt:
         raise ValueError(f"out: type {out.dtype}, x has {x.dtype}")
-    A.apart("out", op, oe, xp, xe)
+    if xp < oe and op < xe:
+        A.overlaps("out")
     rp = None if perm is None else A.whole("perm", perm, dev, _I32, (n,))
     A.launch(_lib().moe_permute, dev, stream, dt, xp, ldx, rp, pp, T, k, n, cols, op, ldo)
 
@@ -101,13 +102,14 @@ def unpermute(y, pos, w, out, base=None, stream=None):
     T, k = shape
     yt, yp, ldy, ye = A.rows("y", y, dev, n, cols)
     ot, op, ldo, oe = A.rows("out", out, dev, T, cols)
-    A.apart("out", op, oe, yp, ye)
+    if yp < oe and op < ye:
+        A.overlaps("out")
     wp = None if w is None else A.whole("w", w, dev, _F32, shape)
     bp, ldb = None, 0
     if base is not None:
         _, bp, ldb, be = A.rows("base", base, dev, T, cols, A.F32_ONLY)
-        if bp != op or ldb != ldo or ot != B.MOE_T_F32:       # else in place
-            A.apart("out", op, oe, bp, be)
+        if bp < oe and op < be and (bp != op or ldb != ldo or ot != B.MOE_T_F32):       # else in place
+            A.overlaps("out")
     A.launch(_lib().moe_unpermute, dev, stream, yt, yp, ldy, n, pp, wp, bp, ldb, T, k, cols, ot, op, ldo)
 
 
@@ -129,8 +131,8 @@ an unpermute without weights dy is permute(dout)."""
     dt, dp, lddy, de = A.rows("dy", dy, dev, n, cols)
     if dt != yt:
         raise ValueError(f"dy: type {dy.dtype}, y has {y.dtype}")
-    A.apart("dy", dp, de, yp, ye)
-    A.apart("dy", dp, de, gp, ge)
+    if (yp < de and dp < ye) or (gp < de and dp < ge):
+        A.overlaps("dy")
     rp = None if perm is None else A.whole("perm", perm, dev, _I32, (n,))
     A.launch(_lib().moe_unpermute_backward, dev, stream, ot, gp, ldd, yt, yp, ldy, rp, n, pp,
              A.whole("w", w, dev, _F32, shape), T, k, cols, dp, lddy, A.whole("dw", dw, dev, _F32, shape))
@@ -143,7 +145,7 @@ def gate_backward(ids, w, dw, dlogits, stream=None):
     ip, shape = _tokens("ids", ids, dev)
     T, k = shape
     _, zp, ldz, ze = A.rows("dlogits", dlogits, dev, T, E, A.F32_ONLY)
-    wp, dp = A.whole("w", w, dev, _F32, shape), A.whole("dw", dw, dev, _F32, shape)
-    A.apart("dlogits", zp, ze, wp, wp + 4 * T * k)
-    A.apart("dlogits", zp, ze, dp, dp + 4 * T * k)
+    wp, dp, size = A.whole("w", w, dev, _F32, shape), A.whole("dw", dw, dev, _F32, shape), 4 * T * k
+    if (wp < ze and zp < wp + size) or (dp < ze and zp < dp + size):
+        A.overlaps("dlogits")
     A.launch(_lib().moe_gate_backward, dev, stream, ip, wp, dp, T, k, E, zp, ldz)

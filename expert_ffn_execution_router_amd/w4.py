@@ -26,9 +26,8 @@ _X = {torch.bfloat16: B.MOE_T_BF16, torch.float16: B.MOE_T_F16}
 _I32 = torch.int32
 
 
-def _matmul(x, out, codes, scales, zeros, gated, E, row_map, map_div, offsets, counts, n, stream):
-    dev, K = x.get_device(), x.shape[-1]
-    lead, sshape = codes.shape[:-1], scales.shape
+def _matmul(x, dev, xshape, out, codes, scales, zeros, gated, E, row_map, map_div, offsets, counts, n, stream):
+    K, lead, sshape = xshape[-1], codes.shape[:-1], scales.shape
     xt, xp, ldx, xe = A.rows("x", x, dev, None, K, _X)
     groups, st = sshape[-1], _X.get(scales.dtype)
     if sshape[:-1] != lead or groups < 1 or K % groups:
@@ -37,11 +36,12 @@ def _matmul(x, out, codes, scales, zeros, gated, E, row_map, map_div, offsets, c
         raise ValueError(f"scales: type {scales.dtype}, expected bf16 or fp16")
     N = lead[-1]
     cp = A.whole("codes", codes, dev, torch.uint8, (*lead, K // 2))
-    sp = A.whole("scales", scales, dev, scales.dtype, sshape)
+    sp = A.whole("scales", scales, dev, scales.dtype)
     zp = None if zeros is None else A.whole("zeros", zeros, dev, x.dtype, sshape)
     ot, op, ldo, oe = A.rows("out", out, dev, n, N // 2 if gated else N)
-    A.apart("out", op, oe, xp, xe)
-    A.launch(B.lib().moe_w4_matmul, dev, stream, xt, xp, ldx, x.shape[0], row_map, map_div, offsets, counts, E, n, cp,
+    if xp < oe and op < xe:
+        A.overlaps("out")
+    A.launch(B.lib().moe_w4_matmul, dev, stream, xt, xp, ldx, xshape[0], row_map, map_div, offsets, counts, E, n, cp,
              st, sp, zp, N, K, K // groups, 1 if gated else 0, ot, op, ldo)
 
 
@@ -49,7 +49,8 @@ def linear(x, out, codes, scales, zeros=None, gated=False, stream=None):
     """out = x W^T for x [T, K] and one matrix (codes [N, K/2])."""
     if codes.dim() != 2:
         raise ValueError(f"codes: shape {tuple(codes.shape)}, expected [N, K/2]")
-    _matmul(x, out, codes, scales, zeros, gated, 1, None, 1, None, None, x.shape[0], stream)
+    shape = x.shape
+    _matmul(x, x.get_device(), shape, out, codes, scales, zeros, gated, 1, None, 1, None, None, shape[0], stream)
 
 
 def experts(x, offsets, out, codes, scales, zeros=None, counts=None, row_map=None, map_div=1, gated=False,
@@ -62,10 +63,10 @@ def experts(x, offsets, out, codes, scales, zeros=None, counts=None, row_map=Non
         raise ValueError(f"codes: shape {tuple(codes.shape)}, expected [E, N, K/2]")
     if map_div >> 31:
         raise ValueError(f"map_div: {map_div}, need 1 <= map_div < 2^31")
-    dev, E, n = x.get_device(), codes.shape[0], out.shape[0]
+    dev, shape, E, n = x.get_device(), x.shape, codes.shape[0], out.shape[0]
     op = A.whole("offsets", offsets, dev, _I32, (E + 1,))
     cp = None if counts is None else A.whole("counts", counts, dev, _I32, (E,))
     mp = None if row_map is None else A.whole("row_map", row_map, dev, _I32, (n,))
-    if row_map is None and x.shape[0] < n:
-        raise ValueError(f"x: {x.shape[0]} rows, out has {n}")
-    _matmul(x, out, codes, scales, zeros, gated, E, mp, map_div, op, cp, n, stream)
+    if row_map is None and shape[0] < n:
+        raise ValueError(f"x: {shape[0]} rows, out has {n}")
+    _matmul(x, dev, shape, out, codes, scales, zeros, gated, E, mp, map_div, op, cp, n, stream)
