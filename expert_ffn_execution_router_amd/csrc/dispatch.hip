@@ -207,10 +207,14 @@ sort_scan_kernel(int32_t* __restrict__ hist, int nblk, int E) {
 // by value.  Units need no alignment beyond the value's.  tpr threads (a
 // power of two up to 256) move a row, 256 / tpr rows to a workgroup; at 256 a
 // row's index is the workgroup's, so its places and weights are read by scalar
-// loads.  HBM bounds all of them: 16384 tokens x 8 copied rows of 6144 bf16
-// take 387 us (1.81 GB), 8192 x 8 combined rows of 2048 59 us (303 MB),
-// gradients of 4096 x 6 rows of 4096 147 us (676 MB), a large copy moving
-// 4.8 TB/s.
+// loads.  HBM bounds the large ones, beside a large copy's 4.8 TB/s: 16384
+// tokens x 8 copied rows of 6144 bf16 391 us (1.81 GB, and 0.2 GB of padding
+// in segments of 128: 5.1 TB/s), 8192 x 8 combined rows of 2048 59 us (303 MB,
+// nine parts in ten read: 5.1 TB/s), gradients of 4096 x 6 rows of 4096 147 us
+// (676 MB in three launches: 4.6 TB/s).  Small ragged ones are bound by
+// latency: gradients of 777 x 5 fp32 rows of 1001 in segments of 16 take 20 us
+// in three launches (45 MB: 2.2 TB/s), half of it in the first, where a
+// padding workgroup waits for one perm entry after the other.
 struct RowMap {
   int tpr_log2;
 };

@@ -229,9 +229,18 @@ DEV void spread_rows(uint32_t v, uint32_t (&o)[4]) {
 // different one; the lane rows then hand them to each other.
 //
 // Codes are loaded without the nontemporal hint: a load takes half of a
-// 128-byte line of each row, the load of the next step the other half, and
-// with the hint the line was fetched twice (72 against 86 us, 64 tokens, 128
-// experts, top-8, 2048 inputs, 1536 gated rows).
+// 128-byte line of each row, the load of the next step the other half.  With
+// weights that rotate past the last-level cache, without against with the
+// hint: 60 against 73 us for 64 rows, 6144 -> 2 x 6144, 46 against 51 us for
+// 64 tokens x 8 of 128 experts, 2048 -> 2 x 768.
+//
+// What bounds it with few rows is vector work and the latency of the codes: a
+// wave spends 39 vector instructions per KB of codes (63 with groups of 64 and
+// zeros) besides the matrix ones, and a tile group's loads are in flight only
+// while the last one's sums are added.  64 tokens x 8 of 128, 2048 -> 2 x 768
+// and 32 tokens x 6 of 256, 2048 -> 4096, groups of 64 with zeros, both stream
+// 3.7 TB/s.  Past 16 rows the codes are converted again for every 16, and past
+// 2048 inputs x, twice the codes' bytes, is read again for every tile group.
 constexpr int MAX_WAVES = 8;
 
 template <int XT, int ST, int GM, int S, bool LONG, bool GATED, bool HZ>
@@ -453,11 +462,18 @@ void launch(const W4Args& a, int otype, hipStream_t s) {
 
 // Two steps of inputs per wave (their group values come in pairs) hold rows of
 // up to 2048; longer rows are taken in passes, the x rows read again for each
-// tile pair: 4096 inputs, 16 rows, 4096 weight rows 9.1 us against 9.9 with
-// four steps held, 6144 inputs, 64 rows, 12288 gated rows 56 against 74 with
-// six (twice the registers, half the waves).  With thousands of pairs holding
-// four steps wins back the x reads: 64 experts, 4096 inputs, 4096 rows 110
-// against 140 us.
+// tile pair.  Rows of up to 4096 can be held with four steps, on half the
+// waves: many tile pairs win that back by not reading x again.  Held against
+// passes in us, weights rotating past the last-level cache, groups of 128:
+//   tile pairs       512      1024       2048       4096       8192
+//   4096 inputs  20 / 18   35 / 28   48 /  52   70 /  98  116 / 191
+//   2176 inputs  15 / 11   25 / 22   34 /  36   51 /  66   86 / 128
+//   64 experts, 32 tokens x 4, 4096 rows (8704 pairs), 4096 inputs: 86 / 110
+// Groups of 32 and 64 cross later and less (4096 inputs, groups of 32: 58 / 53
+// at 2048, 90 / 99 at 4096, 158 / 191 at 8192), hence 4096.  With few rows per
+// expert they go either way past it: 128 experts, 64 tokens x 8, 2176 inputs,
+// groups of 64: 2048 weight rows 111 / 128, with zeros 150 / 145, 4096 with
+// zeros 272 / 235.
 template <int XT, int ST, int GM, bool GATED, bool HZ>
 void choose(const W4Args& a, int otype, hipStream_t s) {
   const int steps = (a.K + 127) / 128;
