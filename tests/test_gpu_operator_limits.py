@@ -46,6 +46,27 @@ def test_neighbours_and_column_ranges_of_one_buffer():
     assert np.array_equal(np64(x), rows)
 
 
+def test_index_and_weight_tensors_are_looked_at():
+    """Through the torch layer, with nothing run: results over places,
+    weights, counts and scales."""
+    print("shared", flush=True)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ids, counts, offsets, perm, pos = (torch.full(s, -1, **i32) for s in ((4, 2), (8,), (9,), (8,), (4, 2)))
+    x, y, w = torch.ones(4, 64, device="cuda"), torch.ones(8, 64, device="cuda"), torch.ones(4, 2, device="cuda")
+    codes, scales = torch.zeros(1, 16, 32, device="cuda", dtype=torch.uint8), torch.ones(1, 16, 2, device="cuda", dtype=BF)
+    calls = [lambda: D.sort(ids, counts, offsets, perm, ids),
+             lambda: D.sort(ids, offsets[1:], offsets, perm, pos),
+             lambda: D.sort(ids, counts, offsets, pos.view(-1), pos),
+             lambda: D.unpermute_backward(x, y, perm, pos, w, torch.empty_like(y), w),
+             lambda: D.unpermute(y[:, :1], pos, w, w[:, :1]),
+             lambda: D.permute(x[:, :1], None, pos, pos.view(torch.float32).view(8, 1)),
+             lambda: w4.linear(x[:1].to(BF), scales.view(1, 32)[:, :16], codes[0], scales[0])]
+    for call in calls:
+        with pytest.raises(B.MoeError, match="shares memory"):
+            call()
+    assert (ids == -1).all() and (pos == -1).all() and (w == 1).all() and (scales == 1).all() and (offsets == -1).all()
+
+
 # E, N, K, group: as few group values as one load of a step reads, or fewer in
 # a matrix of several
 FEWEST = [(1, 1, 128, 32), (1, 2, 64, 32), (2, 1, 64, 32), (3, 1, 64, 32), (5, 1, 96, 32), (4, 1, 32, 32), (1, 1, 32, 32),
