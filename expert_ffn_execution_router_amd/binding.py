@@ -77,7 +77,7 @@ class moe_profile(ctypes.Structure):
 
 
 _vp, _i, _sz, _d = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_double
-_ll = ctypes.c_longlong
+_ll, _f = ctypes.c_longlong, ctypes.c_float
 _P = ctypes.POINTER
 
 # name -> (restype, argtypes), in the order of include/moe.h
@@ -125,6 +125,19 @@ SIGNATURES = {
     "moe_gate_backward": (_i, [_vp, _vp, _vp, _ll, _ll, _ll, _vp, _ll, _vp]),
     "moe_w4_matmul": (_i, [_i, _vp, _ll, _ll, _vp, _ll, _vp, _vp, _ll, _ll, _vp, _i, _vp, _vp, _ll, _ll, _ll, _i, _i,
                            _vp, _ll, _vp]),
+    "moe_fp8_quantize": (_i, [_i, _vp, _ll, _ll, _vp, _ll, _i, _ll, _ll, _vp, _vp, _vp, _vp, _vp]),
+    "moe_fp8_quantize_weights": (_i, [_i, _vp, _ll, _ll, _ll, _vp, _vp, _vp, _vp, _vp]),
+    "moe_gated_backward": (_i, [_i, _vp, _ll, _vp, _ll, _ll, _ll, _vp, _ll, _vp]),
+    "moe_fp8_matmul": (_i, [_vp, _vp, _vp, _vp, _ll, _ll, _vp, _vp, _ll, _ll, _i, _vp, _ll, _vp]),
+    "moe_fp8_weight_gradient": (_i, [_vp, _vp, _vp, _vp, _vp, _ll, _ll, _ll, _ll, _i, _vp, _ll, _vp]),
+    "moe_fp8_layer_workspace_bytes": (_sz, [_ll, _ll, _ll, _ll, _ll]),
+    "moe_fp8_layer": (_i, [_i, _vp, _ll, _vp, _vp, _ll, _ll, _ll, _ll, _ll, _vp, _vp, _vp, _vp, _vp, _ll, _i, _vp,
+                           _ll, _vp, _vp, _vp, _sz, _vp]),
+    "moe_norm": (_i, [_i, _vp, _ll, _i, _vp, _ll, _f, _i, _vp, _i, _vp, _ll, _ll, _vp, _ll, _vp, _vp, _ll, _vp,
+                      _ll, _ll, _f, _f, _vp]),
+    "moe_norm_backward_workspace_bytes": (_sz, [_ll, _ll]),
+    "moe_norm_backward": (_i, [_i, _i, _vp, _ll, _vp, _ll, _f, _i, _vp, _i, _vp, _ll, _ll, _vp, _ll, _vp, _ll, _vp,
+                               _vp, _ll, _vp, _ll, _vp, _i, _vp, _ll, _ll, _vp, _ll, _ll, _f, _f, _vp, _sz, _vp]),
 }
 
 _lib = None
@@ -209,6 +222,16 @@ moe_unpermute = _fn("moe_unpermute")
 moe_unpermute_backward = _fn("moe_unpermute_backward")
 moe_gate_backward = _fn("moe_gate_backward")
 moe_w4_matmul = _fn("moe_w4_matmul")
+moe_fp8_quantize = _fn("moe_fp8_quantize")
+moe_fp8_quantize_weights = _fn("moe_fp8_quantize_weights")
+moe_gated_backward = _fn("moe_gated_backward")
+moe_fp8_matmul = _fn("moe_fp8_matmul")
+moe_fp8_weight_gradient = _fn("moe_fp8_weight_gradient")
+moe_fp8_layer_workspace_bytes = _fn("moe_fp8_layer_workspace_bytes")
+moe_fp8_layer = _fn("moe_fp8_layer")
+moe_norm = _fn("moe_norm")
+moe_norm_backward_workspace_bytes = _fn("moe_norm_backward_workspace_bytes")
+moe_norm_backward = _fn("moe_norm_backward")
 
 
 def make_config(L, E, k, H, I, wfmt, n_slots, max_tokens, host_threads=0) -> moe_config:

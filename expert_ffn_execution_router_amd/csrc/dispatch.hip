@@ -11,10 +11,9 @@
 //
 // Every sum is fp32 in a fixed order and every rank is counted, not drawn
 // from an atomic, so equal inputs give equal bits.
-#include "fwd_ws.h"
-#include "moe.h"
+#include "elem.h"
+#include "op_host.h"
 #include "route_dev.h"
-#include "spans.h"
 
 namespace {
 
@@ -230,49 +229,6 @@ DEV int row_of(const RowMap m, long& row) {
 }
 
 constexpr int PAD_ROWS = 16;      // grouped rows a padding workgroup looks over
-
-template <int DT>
-struct Elem;
-template <>
-struct Elem<MOE_T_BF16> {
-  typedef uint16_t type;
-  static DEV float load(uint16_t v) { return bf16_bits_to_f32(v); }
-  static DEV uint16_t store(float v) { return (uint16_t)pack_bf16x2(v, 0.0f); }
-};
-template <>
-struct Elem<MOE_T_F16> {
-  typedef uint16_t type;
-  static DEV float load(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
-  static DEV uint16_t store(float v) { return (uint16_t)pack_f16x2(v, 0.0f); }
-};
-template <>
-struct Elem<MOE_T_F32> {
-  typedef float type;
-  static DEV float load(float v) { return v; }
-  static DEV float store(float v) { return v; }
-};
-
-// V values, aligned as one is.
-template <typename T, int V>
-struct Pack {
-  T v[V];
-};
-
-template <int DT, int V>
-DEV void load_vals(const typename Elem<DT>::type* p, float (&f)[V]) {
-  Pack<typename Elem<DT>::type, V> a;
-  __builtin_memcpy(&a, p, sizeof(a));
-#pragma unroll
-  for (int i = 0; i < V; ++i) f[i] = Elem<DT>::load(a.v[i]);
-}
-
-template <int DT, int V>
-DEV void store_vals(typename Elem<DT>::type* p, const float (&f)[V]) {
-  Pack<typename Elem<DT>::type, V> a;
-#pragma unroll
-  for (int i = 0; i < V; ++i) a.v[i] = Elem<DT>::store(f[i]);
-  __builtin_memcpy(p, &a, sizeof(a));
-}
 
 // The value is in registers here (else each store's branch loads it again).
 template <typename T, int V>
@@ -499,20 +455,6 @@ gate_bwd_kernel(const int32_t* __restrict__ ids, const float* __restrict__ w, co
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-int bad(int code, const char* msg) {
-  moe_set_thread_error(msg);
-  return code;
-}
-
-int launched() {
-  const hipError_t e = hipGetLastError();
-  return e == hipSuccess ? MOE_OK : bad(MOE_E_HIP, hipGetErrorString(e));
-}
-
-int shared() { return bad(MOE_E_INVAL, "an output shares memory with an input or another output"); }
-
-int elem_bytes(int dt) { return dt == MOE_T_F32 ? 4 : (dt == MOE_T_BF16 || dt == MOE_T_F16 ? 2 : 0); }
-
 // Threads per row for `units` units, and the workgroups for T rows.
 RowMap row_map_for(int units, long T, long* blocks) {
   int l = 0;
@@ -521,9 +463,7 @@ RowMap row_map_for(int units, long T, long* blocks) {
   return RowMap{l};
 }
 
-constexpr long MAX_BLOCKS = (1L << 24) - 1;     // of 256 threads: a launch holds fewer than 2^32
 constexpr int MAX_K = 64;
-constexpr int64_t I32_MAX = 0x7fffffff;
 
 long sort_blocks(long n) { return n <= SORT_SPAN ? 1 : (n + SORT_SPAN - 1) / SORT_SPAN; }
 

@@ -1,0 +1,266 @@
+// Values to E4M3 codes with a scale for each group of 128 (rows, the same
+// transposed, blocks of weights), and the gradient of silu(gate) * up.
+#include "e4m3.h"
+#include "op_host.h"
+
+namespace {
+
+struct QuantArgs {
+  const void* x;
+  int64_t ldx, x_rows, x_step;     // x_step: values from one matrix to the next (weights)
+  const int32_t* row_map;
+  int map_div;
+  int64_t R, K;
+  uint8_t* codes;                  // [R][Kp]
+  float* scales;                   // rows: [Kp/128][R]; weights: [Rp/128][Kp/128]
+  uint8_t* codes_t;                // [K][Rp]
+  float* scales_t;                 // rows: [Rp/128][K]; weights: [Kp/128][Rp/128]
+  int row_tiles, col_tiles;
+};
+
+enum { Q_ROWS = 1, Q_COLS = 2, Q_BLOCKS = 4 };
+
+// A workgroup takes 128 x 128 values: thread (q, l) = (tid / 16, tid % 16)
+// holds rows 8q .. 8q+7 of columns 8l .. 8l+7, so a row's group is a row of 16
+// lanes and a column's eight codes of a thread are eight bytes of the
+// transposed row.
+template <int DT, int MODE, bool GATED>
+__global__ void __launch_bounds__(256)
+quant_kernel(QuantArgs a) {
+  typedef typename Elem<DT>::type T;
+  __shared__ uint32_t part[4][128];
+  const int tid = threadIdx.x, q = tid >> 4, l = tid & 15, wave = tid >> 6;
+  const int ct = blockIdx.x % a.col_tiles, rest = blockIdx.x / a.col_tiles;
+  const int rt = rest % a.row_tiles, e = rest / a.row_tiles;
+  const int64_t r0 = (int64_t)rt * 128 + 8 * q, c0 = (int64_t)ct * 128 + 8 * l;
+  const int64_t Kp = (int64_t)a.col_tiles * 128, Rp = (int64_t)a.row_tiles * 128;
+  const T* x = (const T*)a.x + e * a.x_step;
+  float v[8][8];
+  unsigned keep = 0;               // bit i: row i is written
+  // rows without a branch between their loads
+  int64_t src[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t r = r0 + i;
+    src[i] = -1;
+    if (r < a.R) {
+      int64_t m = r;
+      if (a.row_map) m = a.row_map[r];
+      if (!a.row_map || m >= -1) keep |= 1u << i;
+      if (m >= 0) {
+        if (a.row_map) m = a.map_div ? m / a.map_div : r;
+        if (m < a.x_rows) src[i] = m;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+    if (src[i] >= 0) load8<DT>(x + src[i] * a.ldx, c0, a.K, v[i]);
+  }
+  if (GATED) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float u[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] = 0.0f;
+      if (src[i] >= 0) load8<DT>(x + src[i] * a.ldx + a.K, c0, a.K, u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = silu(v[i][j]) * u[j];
+    }
+  }
+  if (MODE & Q_ROWS) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[i][j]));
+      const GroupScale s = group_scale(row16_max(m));
+      if (!((keep >> i) & 1)) continue;
+      const uint2 w = {codes4(v[i][0], v[i][1], v[i][2], v[i][3], s.inv),
+                       codes4(v[i][4], v[i][5], v[i][6], v[i][7], s.inv)};
+      *(uint2*)(a.codes + (r0 + i) * Kp + c0) = w;
+      if (l == 0) a.scales[(int64_t)ct * a.R + r0 + i] = s.scale;
+    }
+  }
+  if (MODE & Q_COLS) {
+    if (a.row_map && !__syncthreads_or(keep != 0)) return;      // nothing but rows behind the last segment
+    uint32_t m[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      m[j] = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m[j] = max(m[j], abs_bits(v[i][j]));
+      m[j] = max(m[j], (uint32_t)__shfl_xor((int)m[j], 16, 64));
+      m[j] = max(m[j], (uint32_t)__shfl_xor((int)m[j], 32, 64));
+      if ((tid & 63) < 16) part[wave][8 * l + j] = m[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = 8 * l + j;
+      const GroupScale s = group_scale(max(max(part[0][c], part[1][c]), max(part[2][c], part[3][c])));
+      if (c0 + j >= a.K) continue;
+      const uint2 w = {codes4(v[0][j], v[1][j], v[2][j], v[3][j], s.inv),
+                       codes4(v[4][j], v[5][j], v[6][j], v[7][j], s.inv)};
+      *(uint2*)(a.codes_t + (c0 + j) * Rp + r0) = w;
+      if (q == 0) a.scales_t[(int64_t)rt * a.K + c0 + j] = s.scale;
+    }
+  }
+  if (MODE & Q_BLOCKS) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[i][j]));
+    m = row16_max(m);
+    m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+    if ((tid & 63) == 0) part[wave][0] = m;
+    __syncthreads();
+    const GroupScale s = group_scale(max(max(part[0][0], part[1][0]), max(part[2][0], part[3][0])));
+    const int64_t blocks = (int64_t)a.row_tiles * a.col_tiles;
+    if (a.codes) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (r0 + i >= a.R) continue;
+        const uint2 w = {codes4(v[i][0], v[i][1], v[i][2], v[i][3], s.inv),
+                         codes4(v[i][4], v[i][5], v[i][6], v[i][7], s.inv)};
+        *(uint2*)(a.codes + ((int64_t)e * a.R + r0 + i) * Kp + c0) = w;
+      }
+      if (tid == 0) a.scales[e * blocks + (int64_t)rt * a.col_tiles + ct] = s.scale;
+    }
+    if (a.codes_t) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (c0 + j >= a.K) continue;
+        const uint2 w = {codes4(v[0][j], v[1][j], v[2][j], v[3][j], s.inv),
+                         codes4(v[4][j], v[5][j], v[6][j], v[7][j], s.inv)};
+        *(uint2*)(a.codes_t + ((int64_t)e * a.K + c0 + j) * Rp + r0) = w;
+      }
+      if (tid == 0) a.scales_t[e * blocks + (int64_t)ct * a.row_tiles + rt] = s.scale;
+    }
+  }
+}
+
+// dz = [da u s (1 + g (1 - s)), da g s] with s = 1 / (1 + e^-g) of z = [g, u].
+template <int DT>
+__global__ void __launch_bounds__(256)
+gated_backward_kernel(const typename Elem<DT>::type* __restrict__ z, int64_t ldz,
+                      const typename Elem<DT>::type* __restrict__ da, int64_t lda, int64_t R, int64_t I,
+                      typename Elem<DT>::type* __restrict__ dz, int64_t lddz) {
+  const int64_t units = (I + 7) / 8, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t r = at / units, c = (at - r * units) * 8;
+  if (r >= R) return;
+  float g[8], u[8], d[8], dg[8], du[8];
+  load8<DT>(z + r * ldz, c, I, g);
+  load8<DT>(z + r * ldz + I, c, I, u);
+  load8<DT>(da + r * lda, c, I, d);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float s = 1.0f / (1.0f + expf(-g[i]));
+    dg[i] = d[i] * u[i] * (s * (1.0f + g[i] * (1.0f - s)));
+    du[i] = d[i] * (g[i] * s);
+  }
+  store8<DT>(dz + r * lddz, c, I, dg);
+  store8<DT>(dz + r * lddz + I, c, I, du);
+}
+
+template <int MODE, bool GATED>
+int launch_quant(int dt, const QuantArgs& a, int64_t matrices, hipStream_t s) {
+  const int64_t blocks = (int64_t)a.row_tiles * a.col_tiles * matrices;
+  if (dt == MOE_T_BF16) quant_kernel<MOE_T_BF16, MODE, GATED><<<(unsigned)blocks, 256, 0, s>>>(a);
+  else if (dt == MOE_T_F16) quant_kernel<MOE_T_F16, MODE, GATED><<<(unsigned)blocks, 256, 0, s>>>(a);
+  else quant_kernel<MOE_T_F32, MODE, GATED><<<(unsigned)blocks, 256, 0, s>>>(a);
+  return launched();
+}
+
+int64_t pad128(int64_t n) { return (n + 127) / 128 * 128; }
+
+constexpr int64_t MAX_SIZE = 1 << 30;
+
+}  // namespace
+
+extern "C" {
+
+int moe_fp8_quantize(int dtype, const void* x, int64_t ldx, int64_t x_rows, const int32_t* row_map, int64_t map_div,
+                     int gated, int64_t rows, int64_t cols, uint8_t* codes, float* scales, uint8_t* codes_t,
+                     float* scales_t, void* stream) {
+  const int b = elem_bytes(dtype);
+  if (!b) return bad(MOE_E_INVAL, "unknown type");
+  if (rows < 0 || rows > I32_MAX || x_rows < 0) return bad(MOE_E_INVAL, "rows outside [0, 2^31)");
+  if (x_rows > I32_MAX) return bad(MOE_E_UNSUPPORTED, "x has more than 2^31 - 1 rows");
+  if (cols < 1) return bad(MOE_E_INVAL, "need cols >= 1");
+  if (cols > MAX_SIZE || rows > MAX_SIZE) return bad(MOE_E_UNSUPPORTED, "more than 2^30 rows or columns");
+  const int64_t width = gated ? 2 * cols : cols;
+  if (ldx < width) return bad(MOE_E_INVAL, "row stride smaller than the width");
+  if (row_map && (map_div < 0 || map_div > I32_MAX)) return bad(MOE_E_INVAL, "need 0 <= map_div < 2^31");
+  if (!(row_map && map_div) && x_rows < rows) return bad(MOE_E_INVAL, "x has fewer rows than the codes");
+  if (!codes && !codes_t) return bad(MOE_E_INVAL, "neither codes nor codes_t");
+  if (!codes != !scales || !codes_t != !scales_t) return bad(MOE_E_INVAL, "codes and scales come together");
+  if (rows == 0) return MOE_OK;
+  if (x_rows && !x) return bad(MOE_E_INVAL, "null argument");
+  if (((uintptr_t)codes | (uintptr_t)codes_t) % 16) return bad(MOE_E_INVAL, "codes start on 16 bytes");
+  const int64_t Kp = pad128(cols), Rp = pad128(rows);
+  QuantArgs a{x, ldx, x_rows, 0, row_map, row_map ? (int)map_div : 1, rows, cols, codes, scales, codes_t, scales_t,
+              (int)(Rp / 128), (int)(Kp / 128)};
+  if ((int64_t)a.row_tiles * a.col_tiles > MAX_BLOCKS) return bad(MOE_E_UNSUPPORTED, "too many values");
+  if (outputs_shared({span(codes, rows * Kp), span(scales, Kp / 128 * rows * 4), span(codes_t, cols * Rp),
+                      span(scales_t, Rp / 128 * cols * 4)},
+                     {row_span(x, x_rows, width, ldx, b), span(row_map, rows * 4)}))
+    return shared();
+  const hipStream_t s = (hipStream_t)stream;
+  if (!codes_t) return gated ? launch_quant<Q_ROWS, true>(dtype, a, 1, s) : launch_quant<Q_ROWS, false>(dtype, a, 1, s);
+  if (!codes) return gated ? launch_quant<Q_COLS, true>(dtype, a, 1, s) : launch_quant<Q_COLS, false>(dtype, a, 1, s);
+  return gated ? launch_quant<Q_ROWS | Q_COLS, true>(dtype, a, 1, s)
+               : launch_quant<Q_ROWS | Q_COLS, false>(dtype, a, 1, s);
+}
+
+int moe_fp8_quantize_weights(int dtype, const void* w, int64_t E, int64_t N, int64_t K, uint8_t* codes, float* scales,
+                             uint8_t* codes_t, float* scales_t, void* stream) {
+  const int b = elem_bytes(dtype);
+  if (!b) return bad(MOE_E_INVAL, "unknown type");
+  if (E < 1 || E > I32_MAX || N < 1 || K < 1) return bad(MOE_E_INVAL, "need E, N, K >= 1");
+  if (N > MAX_SIZE || K > MAX_SIZE) return bad(MOE_E_UNSUPPORTED, "more than 2^30 rows or columns");
+  if (!codes && !codes_t) return bad(MOE_E_INVAL, "neither codes nor codes_t");
+  if (!codes != !scales || !codes_t != !scales_t) return bad(MOE_E_INVAL, "codes and scales come together");
+  if (!w) return bad(MOE_E_INVAL, "null argument");
+  if (((uintptr_t)codes | (uintptr_t)codes_t) % 16) return bad(MOE_E_INVAL, "codes start on 16 bytes");
+  const int64_t Kp = pad128(K), Np = pad128(N), blocks = Np / 128 * (Kp / 128);
+  if (blocks > MAX_BLOCKS || blocks * E > MAX_BLOCKS) return bad(MOE_E_UNSUPPORTED, "too many values");
+  if (outputs_shared({span(codes, E * N * Kp), span(scales, E * blocks * 4), span(codes_t, E * K * Np),
+                      span(scales_t, E * blocks * 4)},
+                     {span(w, E * N * K * b)}))
+    return shared();
+  const QuantArgs a{w, K, N, N * K, nullptr, 1, N, K, codes, scales, codes_t, scales_t, (int)(Np / 128),
+                    (int)(Kp / 128)};
+  return launch_quant<Q_BLOCKS, false>(dtype, a, E, (hipStream_t)stream);
+}
+
+int moe_gated_backward(int dtype, const void* z, int64_t ldz, const void* da, int64_t lda, int64_t rows, int64_t I,
+                       void* dz, int64_t lddz, void* stream) {
+  const int b = elem_bytes(dtype);
+  if (!b) return bad(MOE_E_INVAL, "unknown type");
+  if (rows < 0 || rows > I32_MAX) return bad(MOE_E_INVAL, "rows outside [0, 2^31)");
+  if (I < 1) return bad(MOE_E_INVAL, "need a width of at least 1");
+  if (I > MAX_SIZE) return bad(MOE_E_UNSUPPORTED, "rows wider than 2^30");
+  if (ldz < 2 * I || lda < I || lddz < 2 * I) return bad(MOE_E_INVAL, "row stride smaller than the width");
+  if (rows == 0) return MOE_OK;
+  if (!z || !da || !dz) return bad(MOE_E_INVAL, "null argument");
+  const int64_t blocks = (rows * ((I + 7) / 8) + 255) / 256;
+  if (blocks > MAX_BLOCKS) return bad(MOE_E_UNSUPPORTED, "too many values");
+  if (outputs_shared({row_span(dz, rows, 2 * I, lddz, b)},
+                     {row_span(z, rows, 2 * I, ldz, b), row_span(da, rows, I, lda, b)}))
+    return shared();
+#define GO(D)                                                                                                       \
+  gated_backward_kernel<D><<<(unsigned)blocks, 256, 0, (hipStream_t)stream>>>(                                      \
+      (const Elem<D>::type*)z, ldz, (const Elem<D>::type*)da, lda, rows, I, (Elem<D>::type*)dz, lddz)
+  if (dtype == MOE_T_BF16) GO(MOE_T_BF16);
+  else if (dtype == MOE_T_F16) GO(MOE_T_F16);
+  else GO(MOE_T_F32);
+#undef GO
+  return launched();
+}
+
+}  // extern "C"

@@ -459,8 +459,9 @@ int moe_profile_begin(moe_ctx* ctx, int max_launches, unsigned stage_mask);
 int moe_profile_end(moe_ctx* ctx, moe_profile* out);
 
 /* ------------------------------------------------------------------------
- * Operators of their own: expert dispatch with its gradients, and products
- * with 4-bit weights.  No context; every pointer is device memory; sizes,
+ * Operators of their own: expert dispatch with its gradients, products with
+ * 4-bit weights, block-scaled 8-bit quantisation, products and gradients, the
+ * layer of a few tokens, and the norms around a block.  No context; every pointer is device memory; sizes,
  * types and strides are checked on the host before any device work (message
  * in moe_last_error(NULL)); sizes are taken in 64 bits, so that none is cut to
  * one that passes.  Rows have a stride (ld*, in elements, at least the width)
@@ -556,6 +557,118 @@ int moe_w4_matmul(int xtype, const void* x, int64_t ldx, int64_t x_rows, const i
                   const int32_t* offsets, const int32_t* counts, int64_t E, int64_t rows, const uint8_t* codes,
                   int stype, const void* scales, const void* zeros, int64_t N, int64_t K, int64_t group, int gated,
                   int otype, void* out, int64_t ldo, void* stream);
+
+/* Values as E4M3 codes with one fp32 scale per group of 128: with a = max(the
+ * group's largest |v|, 2^-100), scale = a / 448 and code = E4M3(v * (448 / a)),
+ * both quotients and the product rounded to fp32, the code to the nearest
+ * even.  A group that holds an infinity or NaN has a scale and codes whose
+ * products are NaN.  Widths are padded to whole groups, P(n) = n rounded up to
+ * a multiple of 128, with codes of zero; codes start on 16 bytes.
+ *   rows:       codes [rows][P(cols)], scales [P(cols)/128][rows]
+ *   transposed: codes_t [cols][P(rows)], scales_t [P(rows)/128][cols] (groups
+ *               of 128 rows; the operand of a weight gradient)
+ * Either pair may be NULL.  Values: x [x_rows, cols] (MOE_T_*); gated != 0:
+ * silu(x[:, :cols]) * x[:, cols:] of rows of 2 cols.  row_map (int32 [rows] or
+ * NULL): row r is x row row_map[r] / map_div (moe_sort's perm with map_div = k
+ * gathers token rows; map_div 0: x row r itself, for rows that are grouped
+ * already); -1 or a row outside x is a row of zeros, a smaller entry
+ * (moe_sort's -2 behind the last segment) leaves its codes and scales as they
+ * were (transposed: where all 128 rows of a group are such, else zeros).
+ * rows, cols <= 2^30.  INVAL, UNSUPPORTED, HIP. */
+int moe_fp8_quantize(int dtype, const void* x, int64_t ldx, int64_t x_rows, const int32_t* row_map, int64_t map_div,
+                     int gated, int64_t rows, int64_t cols, uint8_t* codes, float* scales, uint8_t* codes_t,
+                     float* scales_t, void* stream);
+
+/* Weights [E][N][K] (contiguous, MOE_T_*) the same way with a scale per block
+ * of 128 x 128: codes [E][N][P(K)], scales [E][P(N)/128][P(K)/128]; transposed
+ * codes_t [E][K][P(N)], scales_t [E][P(K)/128][P(N)/128] (the operand of the
+ * gradient of the rows).  Either pair may be NULL. */
+int moe_fp8_quantize_weights(int dtype, const void* w, int64_t E, int64_t N, int64_t K, uint8_t* codes, float* scales,
+                             uint8_t* codes_t, float* scales_t, void* stream);
+
+/* Gradient of silu(g) * u for z = [g, u] ([rows, 2 I]): dz = [da u silu'(g),
+ * da silu(g)], of one MOE_T_* type. */
+int moe_gated_backward(int dtype, const void* z, int64_t ldz, const void* da, int64_t lda, int64_t rows, int64_t I,
+                       void* dz, int64_t lddz, void* stream);
+
+/* out[r, n] = sum_g a_scales[g, r] w_scales[n / 128, g] sum_{k in group g}
+ * a[r, k] w[n, k]: a [rows][K] and w [E][N][K] as the calls above give them (K
+ * a multiple of 128; P(K) where it was padded), out [rows, N] of any MOE_T_*.
+ *   dense (offsets NULL, E = 1), or per expert: rows offsets[e] .. + counts[e]
+ *   (counts NULL: up to offsets[e + 1]) use matrix e, offsets int32 [E + 1] and
+ *   counts int32 [E] as moe_sort gives them; rows in no segment are left as
+ *   they were.
+ * The group sums are scaled and added in fp32.  Inside a group, fp32 outputs
+ * and calls of few rows take exact products and fp32 sums; 16-bit outputs of
+ * many rows take the 8-bit matrix instruction, whose sum of 128 products keeps
+ * about 2^-16 of their magnitude.  The gradient of a is this call with the
+ * transposed weights.  E <= 1024, N K <= 2^40.  INVAL, UNSUPPORTED, HIP. */
+int moe_fp8_matmul(const uint8_t* a, const float* a_scales, const int32_t* offsets, const int32_t* counts, int64_t E,
+                   int64_t rows, const uint8_t* w, const float* w_scales, int64_t N, int64_t K, int otype, void* out,
+                   int64_t ldo, void* stream);
+
+/* dw[n, k] = sum_G dy_scales[G, n] x_scales[G, k] sum_{r in group G} dy_t[n, r]
+ * x_t[k, r]: both operands transposed and padded as moe_fp8_quantize gives
+ * them for `rows` rows, dw fp32 [E][N][K] with row stride ldw, written whole,
+ * or added to (add != 0).  offsets (int32 [E + 1], multiples of 128, as
+ * moe_sort gives them with align = 128, or NULL with E = 1): matrix e sums the
+ * rows offsets[e] .. offsets[e + 1]; one without rows gets zeros. */
+int moe_fp8_weight_gradient(const uint8_t* dy_t, const float* dy_scales, const uint8_t* x_t, const float* x_scales,
+                            const int32_t* offsets, int64_t E, int64_t rows, int64_t N, int64_t K, int add, float* dw,
+                            int64_t ldw, void* stream);
+
+/* A whole MoE layer for T <= 16 tokens in two kernels: router logits z = x
+ * router^T + bias (fp32), top-k (larger first, ties to the lower expert) and
+ * softmax over the chosen logits, silu(gate) * up and down products of the
+ * chosen experts, out[t] = base[t] + sum_j w[t, j] y (fp32, in expert order,
+ * rounded once).  x bf16 or fp16 [T, H] on 16 bytes, stride a multiple of 8;
+ * router fp32 [E, H], bias fp32 [E] or NULL; gate_up codes [E][2 I][H] (gate
+ * rows first) and down codes [E][H][I] with block scales as
+ * moe_fp8_quantize_weights gives them; base fp32 [T, H] or NULL; out x's type
+ * or fp32; ids int32 and w fp32 [T, k] are outputs.  Weights are met by the
+ * 16-bit rows, activations between the products keep 24 bits.  E <= 256, k <=
+ * 8, H and I multiples of 128 up to 32768.  ws: the workspace bytes below, on
+ * 16 bytes; it holds nothing between calls, and two calls that may run at the
+ * same time need one each. */
+size_t moe_fp8_layer_workspace_bytes(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I);
+int moe_fp8_layer(int xtype, const void* x, int64_t ldx, const float* router, const float* bias, int64_t T, int64_t E,
+                  int64_t k, int64_t H, int64_t I, const uint8_t* gate_up, const float* gate_up_scales,
+                  const uint8_t* down, const float* down_scales, const float* base, int64_t ldb, int otype, void* out,
+                  int64_t ldo, int32_t* ids, float* w, void* ws, size_t ws_bytes, void* stream);
+
+/* The norms around a block, with its gate and residual scale:
+ *   h    = alpha residual + gate * (y / rms(y)) weight, rms(v) = sqrt(mean v^2 + eps)
+ *   next = (h / rms(h)) next_weight                     (with next_eps)
+ * y and next [T, cols] have dtype, residual and h rtype (dtype or fp32);
+ * weights [cols] have wtype, the gate gtype (each dtype or fp32).  h is rounded
+ * once and next is the norm of what is stored.  May be NULL: y (the norm
+ * before a block: h is the residual times alpha), residual (zero), weight (y
+ * as it is), gate (ones), h or next (not written; without h nothing is
+ * rounded).  h may be the residual itself, of one stride.  The gate's strides
+ * are in elements: gate_col 1 or 0 (a value per row), gate_row 0 (a value per
+ * column) or at least cols (at least 1 with gate_col 0).  next_scales (fp32
+ * [P(cols)/128][T] or NULL): next holds E4M3 codes as moe_fp8_quantize makes
+ * them, rows of P(cols) on 8 bytes (ldn in bytes).  cols <= 16384. */
+int moe_norm(int dtype, const void* y, int64_t ldy, int rtype, const void* residual, int64_t ldr, float alpha,
+             int wtype, const void* weight, int gtype, const void* gate, int64_t gate_row, int64_t gate_col, void* h,
+             int64_t ldh, const void* next_weight, void* next, int64_t ldn, float* next_scales, int64_t T,
+             int64_t cols, float eps, float next_eps, void* stream);
+
+/* Gradients of moe_norm.  dh (rtype) is the gradient of h, dnext (dtype) that
+ * of next; either may be NULL.  With dnext: h as it was written and
+ * next_weight.  With y: dy (dtype) is required, and weight and gate are what
+ * the call had.  dr (rtype, may be NULL) = alpha times the whole gradient of h.
+ * dweight and dnext_weight fp32 [cols], written whole, may be NULL; dgate
+ * (dtype or fp32, may be NULL) has the gate's shape and is summed over what the
+ * gate was spread over.  ws: the workspace bytes below, on 4 bytes, where a sum
+ * over the rows is asked for. */
+size_t moe_norm_backward_workspace_bytes(int64_t T, int64_t cols);
+int moe_norm_backward(int dtype, int rtype, const void* dh, int64_t lddh, const void* y, int64_t ldy, float alpha,
+                      int wtype, const void* weight, int gtype, const void* gate, int64_t gate_row, int64_t gate_col,
+                      const void* dnext, int64_t lddn, const void* h, int64_t ldh, const void* next_weight, void* dy,
+                      int64_t lddy, void* dr, int64_t lddr, float* dweight, int dgtype, void* dgate,
+                      int64_t dgate_row, int64_t dgate_col, float* dnext_weight, int64_t T, int64_t cols, float eps,
+                      float next_eps, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

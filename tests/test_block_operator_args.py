@@ -1,0 +1,318 @@
+"""CPU tests of the block-scaled 8-bit operators, the layer of a few tokens and
+the norms: every refusal of the C ABI happens before device work (no GPU here),
+sizes are as documented and taken in 64 bits, results that share memory and
+tensors that want a graph are refused, and the torch layer refuses wrong types,
+shapes, strides and places."""
+import os
+
+import pytest
+import torch
+
+BF, HF, F8 = torch.bfloat16, torch.float16, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def B():
+    from expert_ffn_execution_router_amd import binding
+    if not os.path.exists(binding.LIB_PATH):
+        from expert_ffn_execution_router_amd.build import build
+        build()
+    return binding
+
+
+# addresses a gigabyte apart: arrays of these calls that start there are apart
+A = [(i + 1) << 30 for i in range(24)]
+CUT = 2 ** 32
+
+
+def quantize(B, dt=0, x=A[0], ldx=256, xr=4, rm=None, md=1, gated=0, rows=4, cols=256, c=A[1], s=A[2], ct=A[3], st=A[4]):
+    return B.moe_fp8_quantize(dt, x, ldx, xr, rm, md, gated, rows, cols, c, s, ct, st, None)
+
+
+def weights(B, dt=0, w=A[0], E=2, N=130, K=200, c=A[1], s=A[2], ct=A[3], st=A[4]):
+    return B.moe_fp8_quantize_weights(dt, w, E, N, K, c, s, ct, st, None)
+
+
+def gated(B, dt=0, z=A[0], ldz=64, da=A[1], lda=32, rows=4, I=32, dz=A[2], lddz=64):
+    return B.moe_gated_backward(dt, z, ldz, da, lda, rows, I, dz, lddz, None)
+
+
+def matmul(B, a=A[0], sa=A[1], off=A[2], cnt=A[3], E=2, rows=4, w=A[4], sw=A[5], N=32, K=256, ot=0, out=A[6], ldo=32):
+    return B.moe_fp8_matmul(a, sa, off, cnt, E, rows, w, sw, N, K, ot, out, ldo, None)
+
+
+def gradient(B, dy=A[0], sy=A[1], x=A[2], sx=A[3], off=A[4], E=2, rows=256, N=32, K=48, add=0, dw=A[5], ldw=48):
+    return B.moe_fp8_weight_gradient(dy, sy, x, sx, off, E, rows, N, K, add, dw, ldw, None)
+
+
+def layer(B, xt=0, x=A[0], ldx=256, R=A[1], bias=A[2], T=4, E=8, k=2, H=256, I=128, gu=A[3], sgu=A[4], dn=A[5], sdn=A[6],
+          base=A[7], ldb=256, ot=0, out=A[8], ldo=256, ids=A[9], w=A[10], ws=A[11], wsb=1 << 24):
+    return B.moe_fp8_layer(xt, x, ldx, R, bias, T, E, k, H, I, gu, sgu, dn, sdn, base, ldb, ot, out, ldo, ids, w, ws, wsb,
+                           None)
+
+
+def norm(B, dt=0, y=A[0], ldy=64, rt=0, r=A[1], ldr=64, alpha=1.0, wt=0, w=A[2], gt=0, g=A[3], gr=64, gc=1, h=A[4],
+         ldh=64, w2=A[5], nx=A[6], ldn=64, ns=None, T=4, cols=64, eps=1e-6, eps2=1e-6):
+    return B.moe_norm(dt, y, ldy, rt, r, ldr, alpha, wt, w, gt, g, gr, gc, h, ldh, w2, nx, ldn, ns, T, cols, eps, eps2,
+                      None)
+
+
+def norm_backward(B, dt=0, rt=0, dh=A[0], lddh=64, y=A[1], ldy=64, alpha=1.0, wt=0, w=A[2], gt=0, g=A[3], gr=0, gc=1,
+                  dn=A[4], lddn=64, h=A[5], ldh=64, w2=A[6], dy=A[7], lddy=64, dr=A[8], lddr=64, dw=A[9], dgt=2,
+                  dg=A[10], dgr=0, dgc=1, dw2=A[11], T=4, cols=64, eps=1e-6, eps2=1e-6, ws=A[12], wsb=1 << 20):
+    return B.moe_norm_backward(dt, rt, dh, lddh, y, ldy, alpha, wt, w, gt, g, gr, gc, dn, lddn, h, ldh, w2, dy, lddy, dr,
+                               lddr, dw, dgt, dg, dgr, dgc, dw2, T, cols, eps, eps2, ws, wsb, None)
+
+
+def refused(B, call, bad, code=None):
+    for kw in bad:
+        assert call(B, **kw) == (B.MOE_E_INVAL if code is None else code), kw
+
+
+def test_quantize_refusals(B):
+    refused(B, quantize, [dict(dt=3), dict(dt=-1), dict(ldx=255), dict(xr=3), dict(xr=-1), dict(rows=-1),
+                          dict(rows=2 ** 31), dict(cols=0), dict(gated=1, ldx=511), dict(rm=A[5], md=-1),
+                          dict(rm=A[5], md=2 ** 31), dict(rm=A[5], md=0, xr=3), dict(c=None), dict(s=None), dict(ct=None),
+                          dict(st=None), dict(c=None, s=None, ct=None, st=None), dict(x=None), dict(c=A[1] + 8),
+                          dict(ct=A[3] + 4)])
+    refused(B, quantize, [dict(cols=2 ** 30 + 1, ldx=2 ** 31), dict(rows=2 ** 30 + 1, xr=2 ** 30 + 1),
+                          dict(rows=2 ** 30, cols=2 ** 20, xr=2 ** 30, ldx=2 ** 20), dict(xr=2 ** 31, rm=A[5])],
+            B.MOE_E_UNSUPPORTED)
+    assert quantize(B, rows=0) == quantize(B, rows=0, x=None, xr=0) == 0
+    refused(B, weights, [dict(dt=7), dict(E=0), dict(N=0), dict(K=0), dict(w=None), dict(c=None), dict(st=None),
+                         dict(c=None, s=None, ct=None, st=None), dict(c=A[1] + 1), dict(ct=A[3] + 8), dict(E=2 ** 31)])
+    refused(B, weights, [dict(N=2 ** 30 + 1), dict(K=2 ** 30 + 1), dict(N=2 ** 30, K=2 ** 30), dict(E=2 ** 24)],
+            B.MOE_E_UNSUPPORTED)
+    refused(B, gated, [dict(dt=3), dict(ldz=63), dict(lda=31), dict(lddz=63), dict(rows=-1), dict(I=0), dict(z=None),
+                       dict(da=None), dict(dz=None), dict(rows=2 ** 31)])
+    refused(B, gated, [dict(I=2 ** 30 + 1, ldz=2 ** 32, lda=2 ** 32, lddz=2 ** 32),
+                       dict(rows=2 ** 30, I=64, ldz=128, lda=64, lddz=128)], B.MOE_E_UNSUPPORTED)
+    assert gated(B, rows=0) == 0
+
+
+def test_product_refusals(B):
+    refused(B, matmul, [dict(ot=3), dict(rows=-1), dict(rows=2 ** 31), dict(E=0), dict(E=1025), dict(N=0), dict(K=0),
+                        dict(K=200), dict(off=None), dict(off=None, E=1), dict(ldo=31), dict(a=None), dict(sa=None),
+                        dict(w=None), dict(sw=None), dict(out=None), dict(a=A[0] + 8), dict(w=A[4] + 8)])
+    refused(B, matmul, [dict(N=2 ** 30 + 1, ldo=2 ** 31), dict(K=2 ** 31), dict(N=2 ** 30, K=2 ** 20, ldo=2 ** 30)],
+            B.MOE_E_UNSUPPORTED)
+    assert matmul(B, rows=0) == matmul(B, rows=0, off=None, cnt=None, E=1) == 0
+    refused(B, gradient, [dict(rows=-1), dict(rows=2 ** 31), dict(E=0), dict(E=1025), dict(off=None), dict(N=0), dict(K=0),
+                          dict(ldw=47), dict(dw=None), dict(dy=None), dict(sy=None), dict(x=None), dict(sx=None),
+                          dict(dy=A[0] + 4), dict(x=A[2] + 8)])
+    refused(B, gradient, [dict(N=2 ** 30 + 1), dict(K=2 ** 30 + 1, ldw=2 ** 31), dict(N=2 ** 30, K=2 ** 20, ldw=2 ** 20),
+                          dict(ldw=2 ** 41), dict(rows=2 ** 30 + 1)], B.MOE_E_UNSUPPORTED)
+
+
+def test_layer_refusals(B):
+    need = B.moe_fp8_layer_workspace_bytes(4, 8, 2, 256, 128)
+    assert 0 < need < 1 << 24
+    for bad in ((17, 8, 2, 256, 128), (-1, 8, 2, 256, 128), (4, 257, 2, 256, 128), (4, 8, 9, 256, 128),
+                (4, 2, 3, 256, 128), (4, 8, 2, 200, 128), (4, 8, 2, 256, 0), (4, 8, 2, 32896, 128), (4 + CUT, 8, 2, 256, 128)):
+        assert B.moe_fp8_layer_workspace_bytes(*bad) == 0, bad
+    refused(B, layer, [dict(xt=2), dict(ot=1), dict(xt=1, ot=0), dict(T=-1), dict(k=0), dict(k=9), dict(E=1), dict(H=200),
+                       dict(I=100), dict(H=0), dict(ldx=255), dict(ldx=260), dict(ldo=255), dict(ldb=255), dict(x=None),
+                       dict(R=None), dict(gu=None), dict(sgu=None), dict(dn=None), dict(sdn=None), dict(out=None),
+                       dict(ids=None), dict(w=None), dict(ws=None), dict(wsb=need - 1), dict(ws=A[11] + 8),
+                       dict(x=A[0] + 8), dict(R=A[1] + 4), dict(gu=A[3] + 8), dict(dn=A[5] + 8)])
+    refused(B, layer, [dict(T=17), dict(E=300), dict(k=9, E=16), dict(H=32896, ldx=32896, ldo=32896, ldb=32896),
+                       dict(I=32896)], B.MOE_E_UNSUPPORTED)
+    assert layer(B, T=0) == 0
+
+
+def test_norm_refusals(B):
+    refused(B, norm, [dict(dt=3), dict(rt=1), dict(dt=2, rt=0), dict(wt=1), dict(gt=1), dict(T=-1), dict(T=2 ** 31),
+                      dict(cols=0), dict(ldy=63), dict(ldr=63), dict(ldh=63), dict(ldn=63), dict(gr=63), dict(gr=-1),
+                      dict(gc=2), dict(gr=0, gc=0), dict(y=None), dict(y=None, w=None, g=None, r=None),
+                      dict(h=None, nx=None), dict(w2=None), dict(eps=-1.0), dict(eps2=float("nan")), dict(ns=A[7]),
+                      dict(ns=A[7], ldn=132), dict(ns=A[7], ldn=128, nx=A[6] + 4), dict(nx=None, ns=A[7])])
+    wide = dict(ldy=20000, ldr=20000, ldh=20000, ldn=20000, gr=20000)
+    refused(B, norm, [dict(cols=16385, **wide), dict(cols=2000, T=2 ** 24, **wide), dict(T=2 ** 26),
+                      dict(cols=5000, T=2 ** 22, **wide)], B.MOE_E_UNSUPPORTED)
+    assert norm(B, T=0) == 0
+    need = B.moe_norm_backward_workspace_bytes(4, 64)
+    assert 0 < need <= 1 << 20
+    for bad in ((-1, 64), (4, 0), (4, 16385), (2 ** 31, 64), (4 + CUT, 64 + CUT)):
+        assert B.moe_norm_backward_workspace_bytes(*bad) == 0, bad
+    refused(B, norm_backward, [dict(dt=5), dict(rt=1), dict(wt=1), dict(gt=1), dict(dgt=1), dict(T=-1), dict(cols=0),
+                               dict(lddh=63), dict(ldy=63), dict(lddn=63), dict(ldh=63), dict(lddy=63), dict(lddr=63),
+                               dict(gc=2), dict(gr=0, gc=0), dict(dgr=64), dict(dgc=0, dgr=1), dict(g=None), dict(y=None),
+                               dict(dh=None, dn=None), dict(dy=None), dict(h=None), dict(w2=None), dict(w=None),
+                               dict(dn=None), dict(eps=-1.0), dict(eps2=float("nan")), dict(ws=None), dict(wsb=need - 1),
+                               dict(ws=A[12] + 2)])
+    refused(B, norm_backward, [dict(cols=16385, lddh=20000, ldy=20000, lddn=20000, ldh=20000, lddy=20000, lddr=20000)],
+            B.MOE_E_UNSUPPORTED)
+
+
+def test_sizes_are_not_cut_to_32_bits(B):
+    """A size whose low 32 bits are a valid one is refused."""
+    far = 2 ** 40
+    for call, sizes, strides in (
+            (quantize, dict(rows=4, cols=256, xr=4), dict(ldx=far)),
+            (weights, dict(E=2, N=130, K=200), {}),
+            (gated, dict(rows=4, I=32), dict(ldz=far, lda=far, lddz=far)),
+            (matmul, dict(E=2, rows=4, N=32, K=256), dict(ldo=far)),
+            (gradient, dict(E=2, rows=256, N=32, K=48), dict(ldw=far)),
+            (layer, dict(T=4, E=8, k=2, H=256, I=128), dict(ldx=far, ldo=far, ldb=far)),
+            (norm, dict(T=4, cols=64), dict(ldy=far, ldr=far, ldh=far, ldn=far, gr=far)),
+            (norm_backward, dict(T=4, cols=64), dict(lddh=far, ldy=far, lddn=far, ldh=far, lddy=far, lddr=far))):
+        for n, v in sizes.items():
+            if call is quantize and n == "rows":
+                continue
+            rc = call(B, **{n: v + CUT}, **strides)
+            assert rc in (B.MOE_E_INVAL, B.MOE_E_UNSUPPORTED), (call.__name__, n, rc)
+    assert quantize(B, rows=4 + CUT, xr=4 + CUT) == B.MOE_E_INVAL
+
+
+def shared(B, call, outputs, inputs, sizes, defaults):
+    """call refuses each output that begins at, or one byte before the end of,
+    an input or another output, with the message of shared memory."""
+    for o in outputs:
+        for other in inputs + outputs:
+            if other == o:
+                continue
+            for p in (defaults[other], (defaults[other] + sizes[other] - 1) // 16 * 16):
+                assert call(B, **{o: p}) == B.MOE_E_INVAL, (call.__name__, o, other)
+                assert "shares memory" in B.last_error(), (call.__name__, o, other)
+
+
+def defaults(call):
+    import inspect
+    return {n: p.default for n, p in inspect.signature(call).parameters.items()}
+
+
+def test_shared_memory_is_refused(B):
+    shared(B, quantize, ["c", "s", "ct", "st"], ["x"], dict(x=2048, c=1024, s=32, ct=256 * 128, st=1024), defaults(quantize))
+    assert quantize(B, rm=A[1], md=1) == quantize(B, rm=A[4] + 16, md=1) == B.MOE_E_INVAL
+    shared(B, weights, ["c", "s", "ct", "st"], ["w"], dict(w=104000, c=66560, s=32, ct=102400, st=32), defaults(weights))
+    shared(B, gated, ["dz"], ["z", "da"], dict(z=512, da=256, dz=512), defaults(gated))
+    shared(B, matmul, ["out"], ["a", "sa", "off", "cnt", "w", "sw"],
+           dict(a=1024, sa=32, off=12, cnt=8, w=16384, sw=16, out=256), defaults(matmul))
+    shared(B, gradient, ["dw"], ["dy", "sy", "x", "sx", "off"],
+           dict(dy=8192, sy=256, x=12288, sx=384, off=12, dw=12288), defaults(gradient))
+    need = B.moe_fp8_layer_workspace_bytes(4, 8, 2, 256, 128)
+    shared(B, layer, ["out", "ids", "w", "ws"], ["x", "R", "bias", "gu", "sgu", "dn", "sdn", "base"],
+           dict(x=2048, R=8192, bias=32, gu=8 * 256 * 256, sgu=8 * 4 * 4, dn=8 * 256 * 128, sdn=8 * 2 * 4, base=4096, out=2048,
+                ids=32, w=32, ws=need), defaults(layer))
+    shared(B, norm, ["h", "nx"], ["y", "w", "g", "w2"], dict(y=512, w=128, g=512, w2=128, h=512, nx=512), defaults(norm))
+    d = defaults(norm)
+    assert norm(B, h=d["r"] + 16) == norm(B, nx=d["r"]) == norm(B, h=d["r"], ldh=72) == B.MOE_E_INVAL
+    assert norm(B, h=d["r"], nx=d["r"] + 128) == B.MOE_E_INVAL and "shares memory" in B.last_error()
+    assert norm(B, ns=d["nx"], ldn=128) == norm(B, ns=d["h"], ldn=128) == B.MOE_E_INVAL
+    back = B.moe_norm_backward_workspace_bytes(4, 64)
+    shared(B, norm_backward, ["dy", "dr", "dw", "dg", "dw2", "ws"], ["dh", "y", "w", "g", "dn", "h", "w2"],
+           dict(dh=512, y=512, w=128, g=128, dn=512, h=512, w2=128, dy=512, dr=512, dw=256, dg=256, dw2=256, ws=back),
+           defaults(norm_backward))
+
+
+def f8(*shape):
+    return torch.zeros(shape, dtype=torch.uint8).view(F8)
+
+
+def tensors():
+    z = torch.zeros
+    i32 = dict(dtype=torch.int32)
+    return dict(x=z(4, 256, dtype=BF), c=f8(4, 256), s=z(2, 4), ct=f8(256, 128), st=z(1, 256), m=z(4, **i32),
+                w=z(2, 130, 200, dtype=BF), wc=f8(2, 130, 256), ws=z(2, 2, 2), wct=f8(2, 200, 256), wst=z(2, 2, 2),
+                zz=z(4, 64, dtype=BF), da=z(4, 32, dtype=BF), dz=z(4, 64, dtype=BF), l=f8(32, 256), ls=z(1, 2),
+                o=z(4, 32, dtype=BF), e=f8(2, 32, 256), es=z(2, 1, 2), off=z(3, **i32), cnt=z(2, **i32), dyt=f8(32, 128),
+                sdy=z(1, 32), dw=z(32, 256), R=z(8, 256), b=z(8), gu=f8(8, 256, 256), sgu=z(8, 2, 2), dn=f8(8, 256, 128),
+                sdn=z(8, 2, 1), out=z(4, 256, dtype=BF), ids=z(4, 2, **i32), p=z(4, 2), base=z(4, 256), nw=z(256, dtype=BF),
+                nw2=z(256, dtype=BF), g=z(4, 1, dtype=BF), h=z(4, 256, dtype=BF), dy=z(4, 256, dtype=BF),
+                dr=z(4, 256, dtype=BF), dnw=z(256), dnw2=z(256), dg=z(4, 1), dn_=z(4, 256, dtype=BF))
+
+
+def calls():
+    from expert_ffn_execution_router_amd import fp8, norms
+    return {
+        "x s st": lambda v: fp8.quantize(v["x"], v["c"], v["s"], v["ct"], v["st"], row_map=v["m"]),
+        "w ws wst": lambda v: fp8.quantize_weights(v["w"], v["wc"], v["ws"], v["wct"], v["wst"]),
+        "zz da dz": lambda v: fp8.gated_backward(v["zz"], v["da"], v["dz"]),
+        "s ls o": lambda v: fp8.linear(v["c"], v["s"], v["l"], v["ls"], v["o"]),
+        "s es o": lambda v: fp8.experts(v["c"], v["s"], v["off"], v["e"], v["es"], v["o"], counts=v["cnt"]),
+        "sdy st dw": lambda v: fp8.weight_gradient(v["dyt"], v["sdy"], v["ct"], v["st"], v["dw"]),
+        "x R sgu sdn out p b base": lambda v: fp8.layer(v["x"], v["R"], v["gu"], v["sgu"], v["dn"], v["sdn"], v["out"],
+                                                        v["ids"], v["p"], bias=v["b"], base=v["base"]),
+        "x nw out": lambda v: norms.before(v["x"], v["nw"], v["out"]),
+        "x nw s": lambda v: norms.before(v["x"], v["nw"], v["c"], scales=v["s"]),
+        "x h out nw g nw2 dn_": lambda v: norms.after(v["x"], v["h"], v["out"], weight=v["nw"], gate=v["g"],
+                                                      next_weight=v["nw2"], next_out=v["dn_"]),
+        "x h nw dr dnw out": lambda v: norms.before_backward(v["x"], v["h"], v["nw"], v["dr"], v["dnw"], base=v["out"]),
+        "x h dy dr nw dnw g dg dn_ out nw2 dnw2": lambda v: norms.after_backward(
+            v["x"], v["h"], v["dy"], v["dr"], weight=v["nw"], dweight=v["dnw"], gate=v["g"], dgate=v["dg"], dnext=v["dn_"],
+            out=v["out"], next_weight=v["nw2"], dnext_weight=v["dnw2"])}
+
+
+def test_torch_layer_takes_what_is_right_and_refuses_the_cpu(B):
+    for names, call in calls().items():
+        with pytest.raises(ValueError, match="on the GPU"):
+            call(tensors())
+
+
+def test_tensors_that_want_a_graph_are_refused(B):
+    for names, call in calls().items():
+        for n in names.split():
+            v = tensors()
+            v[n] = v[n].clone().requires_grad_()
+            with pytest.raises(ValueError, match="requires grad"):
+                call(v)
+            with torch.no_grad(), pytest.raises(ValueError, match="on the GPU"):
+                call(v)
+
+
+def test_torch_layer_refuses(B):
+    """One thing wrong at a time: a type, a shape or strides."""
+    for names, call in calls().items():
+        base = tensors()
+        used = set()
+
+        class Seen(dict):
+            def __getitem__(self, k):
+                used.add(k)
+                return dict.__getitem__(self, k)
+        with pytest.raises(ValueError):
+            call(Seen(base))
+        for n in used:
+            t = base[n]
+            wrong = [t.to(torch.float64) if t.dtype != F8 else t.view(torch.uint8), t[None].repeat(*[1] * (t.dim() + 1)),
+                     t[..., :-1] if t.shape[-1] > 1 else t[:-1]]
+            if t.dim() == 2 and t.shape[0] > 1 and t.shape[1] > 1:
+                wrong.append(t.t())
+                wrong.append(t[:1].expand(t.shape))
+            for x in wrong:
+                with pytest.raises(ValueError) as e:
+                    call(dict(base, **{n: x}))
+                assert "on the GPU" not in str(e.value), (names, n, x.dtype, x.shape)
+
+
+def test_torch_layer_refuses_more(B):
+    from expert_ffn_execution_router_amd import fp8, norms
+    v = tensors()
+
+    def no(fn, *a, match=None, **kw):
+        with pytest.raises(ValueError, match=match):
+            fn(*a, **kw)
+    no(fp8.quantize, v["x"], v["c"], None, match="together")
+    no(fp8.quantize, v["x"], codes_t=v["ct"], match="together")
+    no(fp8.quantize, v["x"][:, :255], v["c"], v["s"], gated=True, match="even")
+    for over in (2 ** 31, CUT + 1, -1):
+        no(fp8.quantize, v["x"], v["c"], v["s"], row_map=v["m"], map_div=over, match="map_div")
+    no(fp8.linear, v["c"][:, :200].contiguous(), v["s"], v["l"], v["ls"], v["o"], match="128")
+    no(fp8.linear, v["c"], v["s"], v["e"], v["es"], v["o"], match="w: shape")
+    no(fp8.experts, v["c"], v["s"], v["off"], v["l"], v["ls"], v["o"], match="w: shape")
+    no(fp8.weight_gradient, v["dyt"], v["sdy"], v["ct"], v["st"], v["dw"], offsets=v["off"], match="dw")
+    no(norms.before, v["x"], v["nw"], v["c"], match="scales")
+    no(norms.before, v["x"], v["nw"], v["out"], scales=v["s"], match="scales")
+    no(norms.before, v["x"], v["nw"], v["out"].float(), match="x")
+    no(norms.before, v["x"], v["nw"].half(), v["out"], match="weight")
+    no(norms.after, v["x"], v["h"], v["out"].float(), match="out")
+    no(norms.after, v["x"], v["h"].half(), v["out"], match="residual")
+    no(norms.after, v["x"], v["h"], v["out"], gate=torch.zeros(1, 1, dtype=BF), match="gate")
+    no(norms.after, v["x"], v["h"], v["out"], gate=torch.zeros(4, 2, dtype=BF), match="gate")
+    no(norms.after, v["x"], v["h"], v["out"], next_out=v["dn_"], match="next_weight")
+    no(norms.after, v["x"], v["h"], v["out"], weight=v["nw"], next_weight=v["nw2"].float(), next_out=v["dn_"],
+       match="next_weight")
+    no(norms.after_backward, None, v["h"], v["dy"], match="dout or dnext")
+    no(norms.after_backward, None, v["h"], v["dy"], dnext=v["dn_"], match="out and next_weight")
+    no(norms.after_backward, v["x"], v["h"], v["dy"], dgate=v["dg"], match="dgate")
+    no(norms.after_backward, v["x"], v["h"], v["dy"], v["dr"].float(), match="dresidual")
