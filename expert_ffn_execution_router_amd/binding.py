@@ -129,7 +129,8 @@ SIGNATURES = {
     "moe_fp8_quantize_weights": (_i, [_i, _vp, _ll, _ll, _ll, _vp, _vp, _vp, _vp, _vp]),
     "moe_gated_backward": (_i, [_i, _vp, _ll, _vp, _ll, _ll, _ll, _vp, _ll, _vp]),
     "moe_fp8_matmul": (_i, [_vp, _vp, _vp, _vp, _ll, _ll, _vp, _vp, _ll, _ll, _i, _vp, _ll, _vp]),
-    "moe_fp8_weight_gradient": (_i, [_vp, _vp, _vp, _vp, _vp, _ll, _ll, _ll, _ll, _i, _vp, _ll, _vp]),
+    "moe_fp8_weight_gradient_workspace_bytes": (_sz, [_ll, _ll, _ll, _ll]),
+    "moe_fp8_weight_gradient": (_i, [_vp, _vp, _vp, _vp, _vp, _ll, _ll, _ll, _ll, _i, _vp, _ll, _vp, _sz, _vp]),
     "moe_fp8_layer_workspace_bytes": (_sz, [_ll, _ll, _ll, _ll, _ll]),
     "moe_fp8_layer": (_i, [_i, _vp, _ll, _vp, _vp, _ll, _ll, _ll, _ll, _ll, _vp, _vp, _vp, _vp, _vp, _ll, _i, _vp,
                            _ll, _vp, _vp, _vp, _sz, _vp]),
@@ -226,6 +227,7 @@ moe_fp8_quantize = _fn("moe_fp8_quantize")
 moe_fp8_quantize_weights = _fn("moe_fp8_quantize_weights")
 moe_gated_backward = _fn("moe_gated_backward")
 moe_fp8_matmul = _fn("moe_fp8_matmul")
+moe_fp8_weight_gradient_workspace_bytes = _fn("moe_fp8_weight_gradient_workspace_bytes")
 moe_fp8_weight_gradient = _fn("moe_fp8_weight_gradient")
 moe_fp8_layer_workspace_bytes = _fn("moe_fp8_layer_workspace_bytes")
 moe_fp8_layer = _fn("moe_fp8_layer")

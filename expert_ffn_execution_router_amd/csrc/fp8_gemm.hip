@@ -6,6 +6,8 @@
 // In both a row operand P (a, dy transposed) with a scale per row and group
 // meets a column operand Q (w, x transposed) with a scale per block of 128 or
 // per column and group; both are summed along their contiguous axis.
+#include <cmath>
+
 #include "e4m3.h"
 #include "op_host.h"
 #include "segments.h"
@@ -27,6 +29,7 @@ struct MmArgs {
   void* out;                   // rows: [R][ldo]; depth: [E][R][ldo]
   int64_t ldo;
   int otype, add;
+  int split;                   // depth: parts of the summed axis, out [E][split][R][ldo]
 };
 
 // 8 codes as fp16, exactly.
@@ -44,88 +47,99 @@ DEV void store_value(void* out, int64_t at, int otype, float v) {
   else ((uint16_t*)out)[at] = Elem<MOE_T_F16>::store(v);
 }
 
-constexpr int SB = 32;         // rows of a workgroup's tile
+// ---------------------------------------------------------------------------
+// few rows
+// ---------------------------------------------------------------------------
+// A workgroup takes 16 columns of Q and up to 16 RT rows of P; its 8 waves
+// share out the groups, read both operands straight into registers (a lane's 16
+// bytes twice per group: whole 128-byte lines of a row) and join their sums in
+// LDS.  The matrix instruction's columns are rows of P and its rows columns of
+// Q, so a lane ends with four neighbours of one row.  The 8-bit instruction's
+// sum of neighbouring products keeps too few bits for fp32 results, and here
+// the weights' bytes are the bound, so the codes are multiplied as fp16, which
+// is exact.
+constexpr int STREAM_WAVES = 8;
 
-// A wave takes 32 rows x 32 columns.  The matrix instruction's columns are
-// rows of P and its rows columns of Q, so a lane ends with four neighbours of
-// one row.  Its sum of 8-bit codes keeps too few bits (measured: 2^-16 of the
-// sum of magnitudes where values are spread), so the codes are multiplied as
-// fp16, which is exact, and summed in fp32.
-template <bool DEPTH>
-__global__ void __launch_bounds__(256)
-mm_simple_kernel(MmArgs a, int row_blocks) {
+template <int RT>
+__global__ void __launch_bounds__(64 * STREAM_WAVES, 2)
+stream_kernel(MmArgs a, int row_blocks) {
+  constexpr int U = RT == 4 ? 2 : 4;             // groups loaded together
+  __shared__ __align__(16) f32x4_t red[STREAM_WAVES][RT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lr = lane & 15, lg = lane >> 4;
-  const int64_t c0 = ((int64_t)blockIdx.x * 4 + wave) * 32;
-  if (c0 >= a.C) return;
+  const int64_t c0 = (int64_t)blockIdx.x * 16;
+  const int G = a.groups;
   for (int blk = blockIdx.y; blk < row_blocks; blk += gridDim.y) {
-    RowBlock b{0, (int64_t)blk * SB, min((int64_t)(blk + 1) * SB, a.R)};
-    int g0 = 0, g1 = a.groups;
-    if (DEPTH) {
-      b.e = blockIdx.z;
-      if (a.offsets) {
-        g0 = min(max(a.offsets[b.e], 0) / 128, a.groups);
-        g1 = min(max(a.offsets[b.e + 1], 0) / 128, a.groups);
+    RowBlock b{0, (int64_t)blk * 16 * RT, min((int64_t)(blk + 1) * 16 * RT, a.R)};
+    if (a.offsets && !find_block<16 * RT>(a.offsets, a.counts, a.E, a.R, blk, b)) return;
+    const uint8_t* q = a.q + ((int64_t)b.e * a.C + min(c0 + lr, a.C - 1)) * a.ldk + 16 * lg;
+    const float* sq = a.sq + ((int64_t)b.e * ((a.C + 127) / 128) + c0 / 128) * G;
+    const uint8_t* p[RT];
+    const float* sp[RT];
+#pragma unroll
+    for (int j = 0; j < RT; ++j) {               // past the last row it again, not stored
+      const int64_t r = min(b.at + 16 * j + lr, b.end - 1);
+      p[j] = a.p + r * a.ldk + 16 * lg;
+      sp[j] = a.sp + r;
+    }
+    f32x4_t acc[RT] = {};
+    i32x4_t qn[U][2];
+    const auto load = [&](int g0) {              // past the last group it again, unused
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t g = min(g0 + u * STREAM_WAVES, G - 1);
+        qn[u][0] = ld16_nt(q + g * 128);
+        qn[u][1] = ld16_nt(q + g * 128 + 64);
       }
-    } else if (a.offsets && !find_block<SB>(a.offsets, a.counts, a.E, a.R, blk, b)) {
-      return;
-    }
-    const uint8_t* q = a.q + (DEPTH ? 0 : b.e * a.C * a.ldk);
-    const int64_t cblocks = (a.C + 127) / 128;
-    const float* sq = a.sq + (DEPTH ? 0 : b.e * cblocks * a.groups);
-    int64_t row[2], col[2];
+    };
+    load(wave);
+    for (int g0 = wave; g0 < G; g0 += STREAM_WAVES * U) {
+      i32x4_t qc[U][2], pv[U][RT][2];
+      float s[U][RT];
+      __builtin_memcpy(qc, qn, sizeof(qc));
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      row[i] = min(b.at + 16 * i + lr, b.end - 1);
-      col[i] = min(c0 + 16 * i + lr, a.C - 1);
-    }
-    f32x4_t acc[2][2] = {};
-    for (int g = g0; g < g1; ++g) {
-      i32x4_t pv[2][2], qv[2][2];
+      for (int u = 0; u < U; ++u) {
+        const int64_t g = min(g0 + u * STREAM_WAVES, G - 1);
+        const float w = sq[g];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          pv[i][h] = ld16(a.p + row[i] * a.ldk + (int64_t)g * 128 + 64 * h + 16 * lg);
-          qv[i][h] = ld16(q + col[i] * a.ldk + (int64_t)g * 128 + 64 * h + 16 * lg);
-        }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {          // columns
-        float sc[4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int64_t c = min(c0 + 16 * i + 4 * lg + v, a.C - 1);
-          sc[v] = DEPTH ? sq[(int64_t)g * a.C + c] : sq[c / 128 * a.groups + g];
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {        // rows
-          f32x4_t s = {};
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int w = 0; w < 2; ++w)
-              s = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(qv[i][h][2 * w], qv[i][h][2 * w + 1]),
-                                                         codes_f16(pv[j][h][2 * w], pv[j][h][2 * w + 1]), s, 0, 0, 0);
-          const float sr = a.sp[(int64_t)g * a.R + row[j]];
-#pragma unroll
-          for (int v = 0; v < 4; ++v) acc[i][j][v] += s[v] * (sc[v] * sr);
+        for (int j = 0; j < RT; ++j) {
+          pv[u][j][0] = ld16(p[j] + g * 128);
+          pv[u][j][1] = ld16(p[j] + g * 128 + 64);
+          s[u][j] = sp[j][g * a.R] * w;
         }
       }
-    }
+      if (g0 + STREAM_WAVES * U < G) load(g0 + STREAM_WAVES * U);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int u = 0; u < U; ++u) {
+        if (g0 + u * STREAM_WAVES >= G) break;
+        f16x8_t m[4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int64_t r = b.at + 16 * j + lr;
+        for (int h = 0; h < 4; ++h) m[h] = codes_f16(qc[u][h >> 1][2 * (h & 1)], qc[u][h >> 1][2 * (h & 1) + 1]);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int64_t c = c0 + 16 * i + 4 * lg + v;
-          if (r >= b.end || c >= a.C) continue;
-          const int64_t at = (DEPTH ? b.e * a.R + r : r) * a.ldo + c;
-          float x = acc[i][j][v];
-          if (DEPTH && a.add) x += ((const float*)a.out)[at];
-          store_value(a.out, at, a.otype, x);
+        for (int j = 0; j < RT; ++j) {
+          f32x4_t pr = {};
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            pr = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                m[h], codes_f16(pv[u][j][h >> 1][2 * (h & 1)], pv[u][j][h >> 1][2 * (h & 1) + 1]), pr, 0, 0, 0);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[j][v] += pr[v] * s[u][j];
         }
       }
+    }
+#pragma unroll
+    for (int j = 0; j < RT; ++j) red[wave][j][lane] = acc[j];
+    __syncthreads();
+    if (wave < RT) {                             // wave j sums the rows 16 j
+      f32x4_t v = {};
+#pragma unroll
+      for (int w = 0; w < STREAM_WAVES; ++w) v += red[w][wave][lane];
+      const int64_t r = b.at + 16 * wave + lr, c = c0 + 4 * lg;
+      if (r < b.end)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (c + u < a.C) store_value(a.out, r * a.ldo + c + u, a.otype, v[u]);
+    }
+    __syncthreads();                             // red is free
   }
 }
 
@@ -147,7 +161,7 @@ struct Tile {
   static constexpr int P_OFF = 0, Q_OFF = BM * 128;
   static constexpr int SP_OFF = Q_OFF + BN * 128;          // scales: 64 floats a wave, 8 waves
   static constexpr int STAGE = SP_OFF + 8 * 256;
-  static constexpr int NST = 3 * STAGE + 4352 <= 160 * 1024 ? 3 : 2;
+  static constexpr int NST = (160 * 1024 - 4352) / STAGE < 6 ? (160 * 1024 - 4352) / STAGE : 6;
   static constexpr int LDS = NST * STAGE;
 };
 constexpr int MAX_E = 1024;
@@ -212,51 +226,58 @@ tile_kernel(MmArgs a) {
     if (tid == 511 && a.E == MAX_E) pref[MAX_E] = nm_all;
     __syncthreads();
   }
-  const int64_t nitems = (int64_t)nm_all * ntiles * (DEPTH ? a.E : 1);
+  const int nitems = nm_all * ntiles * (DEPTH ? a.E * a.split : 1);      // the host looked that it fits
   // each XCD deals its eighth of the list to its workgroups in turn
   constexpr int N_XCD = 8;
   const int xcd = blockIdx.x % N_XCD, per = (gridDim.x + N_XCD - 1 - xcd) / N_XCD;
-  const int64_t it1 = (xcd + 1) * nitems / N_XCD;
-  int64_t it = xcd * nitems / N_XCD + blockIdx.x / N_XCD;
+  const int it1 = (int)((xcd + 1) * (int64_t)nitems / N_XCD);
+  int it = (int)(xcd * (int64_t)nitems / N_XCD) + blockIdx.x / N_XCD;
   if (it >= it1) return;
 
   // The list goes expert by expert, four column tiles at a time over the
   // row tiles, so that workgroups side by side share both.
-  const auto decode = [&](int64_t i, Item& o) {
-    int e = 0, nm = dense_m;
-    int64_t q = i;
-    int64_t first = 0, end = a.R;
+  const auto decode = [&](int i, Item& o) {
+    int e = 0, nm = dense_m, first = 0, end = (int)a.R;
+    unsigned q = i;
     o.g0 = 0;
     o.g1 = a.groups;
     if (DEPTH) {
-      e = (int)(i / ((int64_t)dense_m * ntiles));
-      q = i - (int64_t)e * dense_m * ntiles;
+      e = (int)((unsigned)i / (unsigned)(dense_m * ntiles));
+      q = i - e * dense_m * ntiles;
+      const int x = e / a.split, s = e - x * a.split;      // e: of the outputs
       if (a.offsets) {
-        o.g0 = min(max(a.offsets[e], 0) / 128, a.groups);
-        o.g1 = max(min(max(a.offsets[e + 1], 0) / 128, a.groups), o.g0);
+        o.g0 = min(max(a.offsets[x], 0) / 128, a.groups);
+        o.g1 = max(min(max(a.offsets[x + 1], 0) / 128, a.groups), o.g0);
       }
+      const int64_t n = o.g1 - o.g0;
+      o.g1 = o.g0 + (int)(n * (s + 1) / a.split);
+      o.g0 += (int)(n * s / a.split);
     } else if (a.offsets) {
-      const int m = (int)(i / ntiles);
+      const int m = (int)((unsigned)i / (unsigned)ntiles);
       int hi = a.E - 1;
       while (e < hi) {
         const int mid = (e + hi + 1) >> 1;
         if (pref[mid] <= m) e = mid; else hi = mid - 1;
       }
       nm = pref[e + 1] - pref[e];
-      q = i - (int64_t)pref[e] * ntiles;
-      first = min(max((int64_t)a.offsets[e], (int64_t)0), a.R);
+      q = i - pref[e] * ntiles;
+      first = (int)min(max((int64_t)a.offsets[e], (int64_t)0), a.R);
       const int64_t many = a.counts ? (int64_t)a.counts[e] : (int64_t)a.offsets[e + 1] - a.offsets[e];
-      end = max(min(first + many, a.R), first);
+      end = (int)max(min(first + many, a.R), (int64_t)first);
     }
-    const int quad = (int)(q / (4 * nm)), rest = (int)(q - (int64_t)quad * 4 * nm), wide = min(4, ntiles - 4 * quad);
-    const int mt = rest / wide, nt = 4 * quad + rest - mt * wide;
+    nm = __builtin_amdgcn_readfirstlane(nm);
+    q = __builtin_amdgcn_readfirstlane(q);
+    first = __builtin_amdgcn_readfirstlane(first);
+    end = __builtin_amdgcn_readfirstlane(end);
+    const unsigned quad = q / (4u * nm), rest = q - quad * 4 * nm, wide = min(4, ntiles - 4 * (int)quad);
+    const unsigned mt = rest / wide, nt = 4 * quad + rest - mt * wide;
     // equal tiles of the rows there are
-    const int64_t step = ((end - first + nm - 1) / nm + 15) / 16 * 16;
-    const int64_t r0 = first + mt * step;
+    const unsigned step = (((unsigned)(end - first) + nm - 1) / (unsigned)nm + 15) & ~15u;
+    const int64_t r0 = first + (int64_t)mt * step;
     o.e = __builtin_amdgcn_readfirstlane(e);
-    o.rows = __builtin_amdgcn_readfirstlane((int)max(min(step, end - r0), (int64_t)0));
+    o.rows = (int)max(min((int64_t)step, end - r0), (int64_t)0);
     const int64_t c0 = (int64_t)nt * C::BN;
-    o.cols = __builtin_amdgcn_readfirstlane((int)min((int64_t)C::BN, a.C - c0));
+    o.cols = (int)min((int64_t)C::BN, a.C - c0);
     o.g0 = __builtin_amdgcn_readfirstlane(o.g0);
     o.g1 = __builtin_amdgcn_readfirstlane(o.g1);
     o.r0 = r0;
@@ -378,9 +399,13 @@ tile_kernel(MmArgs a) {
       }
     }
   };
+  // Returns the blocks of 16 rows that the wave stored with NS instructions
+  // each, -1 where their number is another (a ragged edge, sums).
   const auto store = [&](const Item& t) {
+    const int blocks = min(max((t.rows - 16 * SUB * wm + 15) / 16, 0), SUB);
 #pragma unroll
     for (int j = 0; j < SUB; ++j) {
+      if (j >= blocks) break;
       const int r = prow + 16 * j;
       if (r >= t.rows) continue;
       const int64_t at = (DEPTH ? t.e * a.R + t.r0 + r : t.r0 + r) * a.ldo + t.c0;
@@ -393,7 +418,10 @@ tile_kernel(MmArgs a) {
           for (int u = 0; u < 4; ++u)
             if (u < n) v[u] += ((const float*)a.out)[at + c + u];
         if (n >= 4) {
-          if (a.otype == MOE_T_F32) {
+          if (DEPTH) {                               // written once, larger than the caches
+            typedef float f32x4u_t __attribute__((ext_vector_type(4), aligned(4)));
+            __builtin_nontemporal_store(f32x4u_t{v[0], v[1], v[2], v[3]}, (f32x4u_t*)((float*)a.out + at + c));
+          } else if (a.otype == MOE_T_F32) {
             __builtin_memcpy((float*)a.out + at + c, &v, 16);
           } else {
             const uint2 w = a.otype == MOE_T_BF16 ? uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}
@@ -407,6 +435,20 @@ tile_kernel(MmArgs a) {
         }
       }
     }
+    return t.cols == C::BN && !(DEPTH && a.add) ? blocks : -1;
+  };
+  // Loads and stores are counted in the order of issue.  The unit that is
+  // waited for was loaded before `newer` other units and, for NST - 1 units
+  // after an item's end, before its stores: those stay outstanding.
+  // Fewer may stay outstanding than could: near the end, and beside a ragged
+  // item's stores.
+  const auto wait = [&](int newer, int stored) {
+    constexpr int UNITS = (C::LOADS + 1) * (C::NST - 2);
+    static_assert(UNITS + NS * SUB < 64, "the counter's range");
+    if (newer < C::NST - 2) wait_vmcnt<0>();
+    else if (stored >= SUB) wait_vmcnt<UNITS + NS * SUB>();
+    else if (stored >= SUB / 2) wait_vmcnt<UNITS + NS * SUB / 2>();
+    else wait_vmcnt<UNITS>();
   };
 
   // ---- the stream -----------------------------------------------------------
@@ -414,7 +456,7 @@ tile_kernel(MmArgs a) {
   Item cur, nxt;
   decode(it, cur);
   nxt = cur;
-  int64_t nit = it;
+  int nit = it;
   int ng = cur.g0;
   bool more = true;                              // nxt, ng: the next unit to load
   const auto settle = [&] {                      // to an item that has groups
@@ -433,6 +475,7 @@ tile_kernel(MmArgs a) {
   settle();
   clear();
   int ahead = 0, in = 0, out = 0;                // units in flight, stage to fill, stage to read
+  int stored = 0, since = 0;                     // blocks of the last item, units since
   const auto advance = [&] {
     if (!more) return;
     issue(ng, in);
@@ -445,8 +488,8 @@ tile_kernel(MmArgs a) {
   for (int i = 0; i < C::NST - 1; ++i) advance();
   for (;;) {
     for (int g = cur.g0; g < cur.g1; ++g) {
-      if (C::NST == 3 && ahead == 2) wait_vmcnt<C::LOADS + 1>();
-      else wait_vmcnt<0>();
+      wait(ahead - 1, since < C::NST - 1 ? stored : 0);
+      ++since;
       barrier_keep_loads();                      // the unit is there, and the stage before it is free
       __builtin_amdgcn_sched_barrier(0);
       advance();
@@ -454,7 +497,8 @@ tile_kernel(MmArgs a) {
       if (cur.rows > 16 * SUB * wm) compute(lds + out * C::STAGE);
       out = out + 1 == C::NST ? 0 : out + 1;
     }
-    store(cur);
+    stored = max(store(cur), 0);
+    since = 0;
     it += per;
     if (it >= it1) break;
     decode(it, cur);
@@ -463,6 +507,36 @@ tile_kernel(MmArgs a) {
 }
 
 constexpr int64_t MAX_SIZE = 1 << 30, MAX_MATRIX = (int64_t)1 << 40;
+constexpr int CUS = 256;
+
+// Sum of the parts of a split gradient, in their order.
+__global__ void __launch_bounds__(256)
+join_kernel(const float* __restrict__ part, int split, int64_t rows, int64_t R, int64_t C, float* __restrict__ out,
+            int64_t ldo, int add) {
+  const int64_t units = (C + 3) / 4, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = at / units, c = (at - row * units) * 4;
+  if (row >= rows) return;
+  const int64_t e = row / R, r = row - e * R;
+  float v[4] = {};
+  const int n = (int)min((int64_t)4, C - c);
+  for (int s = 0; s < split; ++s) {
+    const float* p = part + ((e * split + s) * R + r) * C + c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) v[i] += p[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < n) out[row * ldo + c + i] = (add ? out[row * ldo + c + i] : 0.0f) + v[i];
+}
+
+template <int RT>
+int launch_stream(const MmArgs& m, hipStream_t s) {
+  const int64_t blocks = (m.R + 16 * RT - 1) / (16 * RT) + (m.offsets ? std::min<int64_t>(m.E, m.R) : 0);
+  const dim3 grid((unsigned)((m.C + 15) / 16), (unsigned)std::min<int64_t>(blocks, 65535));
+  stream_kernel<RT><<<grid, 64 * STREAM_WAVES, 0, s>>>(m, (int)blocks);
+  return launched();
+}
 
 template <bool DEPTH, bool EXACT, int SUB, int NS>
 int launch_tiles(const MmArgs& m, hipStream_t s) {
@@ -471,26 +545,100 @@ int launch_tiles(const MmArgs& m, hipStream_t s) {
                                            hipFuncAttributeMaxDynamicSharedMemorySize, C::LDS);
   if (e != hipSuccess) return bad(MOE_E_HIP, hipGetErrorString(e));
   const int64_t mt = (m.R + C::BM - 1) / C::BM + (!DEPTH && m.offsets ? std::min<int64_t>(m.E, m.R) : 0);
-  const int64_t items = mt * ((m.C + C::BN - 1) / C::BN) * (DEPTH ? m.E : 1);
-  const unsigned grid = (unsigned)std::min<int64_t>((items + 7) / 8 * 8, 256);
+  const int64_t items = mt * ((m.C + C::BN - 1) / C::BN) * (DEPTH ? (int64_t)m.E * m.split : 1);
+  if (items > I32_MAX) return bad(MOE_E_UNSUPPORTED, "too many values");
+  const unsigned grid = (unsigned)std::min<int64_t>((items + 7) / 8 * 8, CUS);
   tile_kernel<DEPTH, EXACT, SUB, NS><<<grid, 512, C::LDS, s>>>(m);
   return launched();
 }
 
-// Tiles of BM x BN of a call.
-int64_t tiles_of(const MmArgs& m, bool depth, int BM, int BN) {
-  return (m.R + BM - 1) / BM * ((m.C + BN - 1) / BN) * (depth ? m.E : 1);
+// What a call would take: rounds of the card's 256 workgroups, times the
+// groups of the summed axis, times what one group takes (ns, measured at 4096
+// columns of Q and groups enough to hide the ends):
+//   tile                    64x128  128x128  128x256  256x256
+//   8-bit instruction          760     1020     1470     2500 (experts 2900)
+//   exact                      930     1330     2150
+//   exact, row scales          890     1350     2050
+//   few rows          16 rows: 190  32: 270  64: 390
+// It is right within a tenth where the rows are (dense, 4096 inputs, us, both
+// sides of each change): 4096 columns, 128 rows: 26 as few rows, 24 as 64x128;
+// 512 rows 25 / 32 as 128x128; 1024 rows 48 as 64x128 / 34 / 46 as 128x256;
+// 2048 rows 65 as 128x128 / 50 / 80 as 256x256; 1024 columns, 512 rows: 25 as
+// few rows, 24 as 64x128.  Experts' rows are expected to fill their last tile
+// by half; 64 experts of about 96 rows, 2048 x 2048: 112 / 97 / 90 / 96; 128 of
+// about 512 rows, unevenly, 1536 x 2048: 400 as 128x256 / 461 as 256x256, which
+// leaves more of its last tiles empty.
+double rounds(double workgroups) { return std::ceil(workgroups / CUS); }
+
+double row_tiles(const MmArgs& m, bool depth, int BM) {
+  if (depth || !m.offsets) return (double)((m.R + BM - 1) / BM);
+  const double act = (double)std::min<int64_t>(m.E, m.R);
+  return act * std::max(1.0, (double)m.R / act / BM + 0.5);
 }
 
-template <bool DEPTH, bool EXACT>
-int choose_tiles(const MmArgs& m, hipStream_t s) {
-  constexpr int CUS = 256;
-  const int64_t per_expert = DEPTH || !m.offsets ? m.R : m.R / m.E;
-  if constexpr (!EXACT)
-    if (per_expert > 192 && tiles_of(m, DEPTH, 256, 256) >= CUS) return launch_tiles<DEPTH, EXACT, 8, 4>(m, s);
-  if (tiles_of(m, DEPTH, 128, 256) >= CUS) return launch_tiles<DEPTH, EXACT, 4, 4>(m, s);
-  if (tiles_of(m, DEPTH, 128, 128) >= CUS) return launch_tiles<DEPTH, EXACT, 4, 2>(m, s);
-  return launch_tiles<DEPTH, EXACT, 2, 2>(m, s);
+double tile_cost(const MmArgs& m, bool depth, int BM, int BN, double ns, double groups) {
+  return rounds(row_tiles(m, depth, BM) * ((m.C + BN - 1) / BN) * (depth ? (double)m.E * m.split : 1.0)) * groups * ns;
+}
+
+int product(const MmArgs& m, hipStream_t s) {
+  const bool exact = m.otype == MOE_T_F32;
+  const double G = m.groups;
+  struct Choice {
+    double cost;
+    int (*launch)(const MmArgs&, hipStream_t);
+  };
+  // few rows of an expert: a workgroup looks its rows up first, about 3 us
+  const auto stream = [&](int rows, double ns) {
+    return rounds(row_tiles(m, false, rows) * ((m.C + 15) / 16)) * (G * ns + (m.offsets ? 3000.0 : 0.0));
+  };
+  const Choice choices[] = {
+      {stream(16, 190), launch_stream<1>},
+      {stream(32, 270), launch_stream<2>},
+      {stream(64, 390), launch_stream<4>},
+      {tile_cost(m, false, 64, 128, exact ? 930 : 760, G), exact ? launch_tiles<false, true, 2, 2> : launch_tiles<false, false, 2, 2>},
+      {tile_cost(m, false, 128, 128, exact ? 1330 : 1020, G), exact ? launch_tiles<false, true, 4, 2> : launch_tiles<false, false, 4, 2>},
+      {tile_cost(m, false, 128, 256, exact ? 2150 : 1470, G), exact ? launch_tiles<false, true, 4, 4> : launch_tiles<false, false, 4, 4>},
+      {exact ? 1e300 : tile_cost(m, false, 256, 256, m.offsets ? 2900 : 2500, G), launch_tiles<false, false, 8, 4>},
+  };
+  const Choice* best = choices;
+  for (const Choice& c : choices)
+    if (c.cost < best->cost) best = &c;
+  return best->launch(m, s);
+}
+
+// Tile and parts of a gradient.  Parts are written and read again, at about
+// 4 bytes a ps.
+struct Depth {
+  int shape, split;
+};
+Depth choose_depth(int64_t E, int64_t N, int64_t K, int64_t rows) {
+  static const struct {
+    int BM, BN;
+    double ns;
+  } shapes[] = {{64, 128, 890}, {128, 128, 1350}, {128, 256, 2050}};
+  MmArgs m{};
+  m.E = (int)E;
+  m.R = N;
+  m.C = K;
+  const double G = std::max(1.0, std::ceil((double)((rows + 127) / 128) / (double)E));      // of an expert
+  Depth best{0, 1};
+  double least = 1e300;
+  for (int split = 1; split <= 16 && split <= G; split *= 2)
+    for (int i = 0; i < 3; ++i) {
+      m.split = split;
+      const double join = split > 1 ? 3000.0 + (2.0 * split + 1) * E * N * K * 4 / 4000.0 : 0.0;
+      const double cost = tile_cost(m, true, shapes[i].BM, shapes[i].BN, shapes[i].ns, std::ceil(G / split)) + join;
+      if (cost < least) {
+        least = cost;
+        best = Depth{i, split};
+      }
+    }
+  return best;
+}
+
+bool gradient_sizes(int64_t E, int64_t rows, int64_t N, int64_t K) {
+  return E >= 1 && E <= MAX_E && rows >= 0 && rows <= MAX_SIZE && N >= 1 && N <= MAX_SIZE && K >= 1 && K <= MAX_SIZE &&
+         N * K <= MAX_MATRIX;
 }
 
 }  // namespace
@@ -517,35 +665,49 @@ int moe_fp8_matmul(const uint8_t* a, const float* a_scales, const int32_t* offse
                      {span(a, rows * K), span(a_scales, G * rows * 4), span(offsets, (E + 1) * 4), span(counts, E * 4),
                       span(w, E * N * K), span(w_scales, E * ((N + 127) / 128) * G * 4)}))
     return shared();
-  const MmArgs m{a, a_scales, w, w_scales, offsets, counts, (int)E, rows, N, K, (int)G, out, ldo, otype, 0};
-  if (rows > 64) return otype == MOE_T_F32 ? choose_tiles<false, true>(m, (hipStream_t)stream) : choose_tiles<false, false>(m, (hipStream_t)stream);
-  // blocks of the segments: one more than the rows fill at most for each expert that has rows
-  const int64_t blocks = (rows + SB - 1) / SB + (offsets ? std::min(E, rows) : 0);
-  const dim3 grid((unsigned)((N + 127) / 128), (unsigned)std::min<int64_t>(blocks, 65535));
-  mm_simple_kernel<false><<<grid, 256, 0, (hipStream_t)stream>>>(m, (int)blocks);
-  return launched();
+  const MmArgs m{a, a_scales, w, w_scales, offsets, counts, (int)E, rows, N, K, (int)G, out, ldo, otype, 0, 1};
+  return product(m, (hipStream_t)stream);
+}
+
+size_t moe_fp8_weight_gradient_workspace_bytes(int64_t E, int64_t rows, int64_t N, int64_t K) {
+  if (!gradient_sizes(E, rows, N, K)) return 0;
+  const int split = choose_depth(E, N, K, rows).split;
+  return split > 1 ? (size_t)split * E * N * K * 4 : 0;
 }
 
 int moe_fp8_weight_gradient(const uint8_t* dy_t, const float* dy_scales, const uint8_t* x_t, const float* x_scales,
                             const int32_t* offsets, int64_t E, int64_t rows, int64_t N, int64_t K, int add, float* dw,
-                            int64_t ldw, void* stream) {
+                            int64_t ldw, void* ws, size_t ws_bytes, void* stream) {
   if (rows < 0 || rows > I32_MAX) return bad(MOE_E_INVAL, "rows outside [0, 2^31)");
-  if (E < 1 || E > 1024) return bad(MOE_E_INVAL, "need 1 <= E <= 1024");
+  if (E < 1 || E > MAX_E) return bad(MOE_E_INVAL, "need 1 <= E <= 1024");
   if (!offsets && E != 1) return bad(MOE_E_INVAL, "without offsets: one matrix");
   if (N < 1 || K < 1) return bad(MOE_E_INVAL, "need N >= 1 and K >= 1");
-  if (N > MAX_SIZE || K > MAX_SIZE || rows > MAX_SIZE) return bad(MOE_E_UNSUPPORTED, "more than 2^30 rows or columns");
-  if (N * K > MAX_MATRIX) return bad(MOE_E_UNSUPPORTED, "a matrix of more than 2^40 values");
+  if (!gradient_sizes(E, rows, N, K))
+    return bad(MOE_E_UNSUPPORTED, "more than 2^30 rows or columns, or a matrix of more than 2^40 values");
   if (ldw < K) return bad(MOE_E_INVAL, "dw's row stride smaller than its width");
   if (ldw > ((int64_t)1 << 40)) return bad(MOE_E_UNSUPPORTED, "dw's row stride over 2^40");
   if (!dw || (rows && (!dy_t || !dy_scales || !x_t || !x_scales))) return bad(MOE_E_INVAL, "null argument");
   if (((uintptr_t)dy_t | (uintptr_t)x_t) % 16) return bad(MOE_E_INVAL, "codes start on 16 bytes");
+  const Depth d = choose_depth(E, N, K, rows);
+  const size_t need = d.split > 1 ? (size_t)d.split * E * N * K * 4 : 0;
+  if (need && (!ws || ws_bytes < need))
+    return bad(MOE_E_INVAL, "workspace smaller than moe_fp8_weight_gradient_workspace_bytes");
+  if (need && (uintptr_t)ws % 4) return bad(MOE_E_INVAL, "the workspace holds floats: it starts on 4 bytes");
   const int64_t Rp = (rows + 127) / 128 * 128, G = Rp / 128;
-  if (outputs_shared({row_span(dw, E * N, K, ldw, 4)},
+  const int64_t join_blocks = (E * N * ((K + 3) / 4) + 255) / 256;
+  if (need && join_blocks > MAX_BLOCKS) return bad(MOE_E_UNSUPPORTED, "too many values");
+  if (outputs_shared({row_span(dw, E * N, K, ldw, 4), span(need ? ws : nullptr, (int64_t)need)},
                      {span(dy_t, N * Rp), span(dy_scales, G * N * 4), span(x_t, K * Rp), span(x_scales, G * K * 4),
                       span(offsets, (E + 1) * 4)}))
     return shared();
-  const MmArgs m{dy_t, dy_scales, x_t, x_scales, offsets, nullptr, (int)E, N, K, Rp, (int)G, dw, ldw, MOE_T_F32, add};
-  return choose_tiles<true, true>(m, (hipStream_t)stream);
+  const hipStream_t s = (hipStream_t)stream;
+  const MmArgs m{dy_t, dy_scales, x_t, x_scales, offsets, nullptr, (int)E, N, K, Rp, (int)G, need ? ws : dw,
+                 need ? K : ldw, MOE_T_F32, need ? 0 : add, d.split};
+  const int rc = d.shape == 0 ? launch_tiles<true, true, 2, 2>(m, s)
+                              : d.shape == 1 ? launch_tiles<true, true, 4, 2>(m, s) : launch_tiles<true, true, 4, 4>(m, s);
+  if (rc || !need) return rc;
+  join_kernel<<<(unsigned)join_blocks, 256, 0, s>>>((const float*)ws, d.split, E * N, N, K, dw, ldw, add);
+  return launched();
 }
 
 }  // extern "C"

@@ -612,10 +612,13 @@ int moe_fp8_matmul(const uint8_t* a, const float* a_scales, const int32_t* offse
  * them for `rows` rows, dw fp32 [E][N][K] with row stride ldw, written whole,
  * or added to (add != 0).  offsets (int32 [E + 1], multiples of 128, as
  * moe_sort gives them with align = 128, or NULL with E = 1): matrix e sums the
- * rows offsets[e] .. offsets[e + 1]; one without rows gets zeros. */
+ * rows offsets[e] .. offsets[e + 1]; one without rows gets zeros.  ws: the
+ * workspace bytes below, on 4 bytes (0 where no long sum is split: ws may be
+ * NULL). */
+size_t moe_fp8_weight_gradient_workspace_bytes(int64_t E, int64_t rows, int64_t N, int64_t K);
 int moe_fp8_weight_gradient(const uint8_t* dy_t, const float* dy_scales, const uint8_t* x_t, const float* x_scales,
                             const int32_t* offsets, int64_t E, int64_t rows, int64_t N, int64_t K, int add, float* dw,
-                            int64_t ldw, void* stream);
+                            int64_t ldw, void* ws, size_t ws_bytes, void* stream);
 
 /* A whole MoE layer for T <= 16 tokens in two kernels: router logits z = x
  * router^T + bias (fp32), top-k (larger first, ties to the lower expert) and

@@ -41,8 +41,9 @@ def matmul(B, a=A[0], sa=A[1], off=A[2], cnt=A[3], E=2, rows=4, w=A[4], sw=A[5],
     return B.moe_fp8_matmul(a, sa, off, cnt, E, rows, w, sw, N, K, ot, out, ldo, None)
 
 
-def gradient(B, dy=A[0], sy=A[1], x=A[2], sx=A[3], off=A[4], E=2, rows=256, N=32, K=48, add=0, dw=A[5], ldw=48):
-    return B.moe_fp8_weight_gradient(dy, sy, x, sx, off, E, rows, N, K, add, dw, ldw, None)
+def gradient(B, dy=A[0], sy=A[1], x=A[2], sx=A[3], off=A[4], E=2, rows=256, N=32, K=48, add=0, dw=A[5], ldw=48, ws=A[6],
+             wsb=1 << 29):
+    return B.moe_fp8_weight_gradient(dy, sy, x, sx, off, E, rows, N, K, add, dw, ldw, ws, wsb, None)
 
 
 def layer(B, xt=0, x=A[0], ldx=256, R=A[1], bias=A[2], T=4, E=8, k=2, H=256, I=128, gu=A[3], sgu=A[4], dn=A[5], sdn=A[6],
@@ -100,6 +101,13 @@ def test_product_refusals(B):
     refused(B, gradient, [dict(rows=-1), dict(rows=2 ** 31), dict(E=0), dict(E=1025), dict(off=None), dict(N=0), dict(K=0),
                           dict(ldw=47), dict(dw=None), dict(dy=None), dict(sy=None), dict(x=None), dict(sx=None),
                           dict(dy=A[0] + 4), dict(x=A[2] + 8)])
+    long = dict(off=None, E=1, rows=65536)
+    need = B.moe_fp8_weight_gradient_workspace_bytes(1, 65536, 32, 48)
+    assert need > 0 and need % (32 * 48 * 4) == 0
+    refused(B, gradient, [dict(ws=None, **long), dict(wsb=need - 1, **long), dict(ws=A[6] + 2, **long)])
+    for bad in ((0, 256, 32, 48), (1025, 256, 32, 48), (1, -1, 32, 48), (1, 256, 0, 48), (1, 256, 32, 2 ** 31),
+                (1 + CUT, 65536, 32, 48)):
+        assert B.moe_fp8_weight_gradient_workspace_bytes(*bad) == 0, bad
     refused(B, gradient, [dict(N=2 ** 30 + 1), dict(K=2 ** 30 + 1, ldw=2 ** 31), dict(N=2 ** 30, K=2 ** 20, ldw=2 ** 20),
                           dict(ldw=2 ** 41), dict(rows=2 ** 30 + 1)], B.MOE_E_UNSUPPORTED)
 

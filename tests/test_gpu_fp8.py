@@ -335,7 +335,7 @@ def test_experts(T, k, E, N, K, align, drop, ot, small):
 
 @pytest.mark.parametrize("small", [True, False])
 @pytest.mark.parametrize("R,N,K", [(1, 1, 1), (5, 40, 130), (128, 128, 128), (300, 257, 100), (1000, 33, 513),
-                                   (130, 300, 520), (0, 7, 9)])
+                                   (130, 300, 520), (0, 7, 9), (5000, 40, 36), (9000, 130, 257)])
 def test_weight_gradient(R, N, K, small):
     print(f"weight gradient R={R} N={N} K={K} small={small}", flush=True)
     rng = np.random.default_rng(R + N + K)
