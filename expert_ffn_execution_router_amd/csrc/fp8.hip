@@ -21,62 +21,85 @@ struct QuantArgs {
 enum { Q_ROWS = 1, Q_COLS = 2, Q_BLOCKS = 4 };
 
 // A workgroup takes 128 x 128 values: thread (q, l) = (tid / 16, tid % 16)
-// holds rows 8q .. 8q+7 of columns 8l .. 8l+7, so a row's group is a row of 16
-// lanes and a column's eight codes of a thread are eight bytes of the
-// transposed row.
+// holds rows 4q .. 4q+3 of columns 8l .. 8l+7, so a row's group is a row of 16
+// lanes and a column's four codes of a thread are a word of the transposed
+// row.  Transposed codes pass through LDS, so that whole rows of 128 bytes are
+// stored: the 16-byte pieces of column c are XORed with c / 8, which spreads
+// the words that a wave writes over the banks.
+constexpr int Q_THREADS = 512, Q_SPAN = 4;       // rows of a thread
+
+DEV int tile_word(int c, int q) { return c * 32 + (((q >> 2) ^ (c >> 3)) & 7) * 4 + (q & 3); }
+
 template <int DT, int MODE, bool GATED>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(Q_THREADS)
 quant_kernel(QuantArgs a) {
   typedef typename Elem<DT>::type T;
-  __shared__ uint32_t part[4][128];
+  constexpr int WAVES = Q_THREADS / 64, S = Q_SPAN;
+  __shared__ uint32_t part[WAVES][128];
+  __shared__ __align__(16) uint32_t tile[(MODE & Q_ROWS) && !(MODE & Q_COLS) ? 4 : 128 * 32];
   const int tid = threadIdx.x, q = tid >> 4, l = tid & 15, wave = tid >> 6;
-  const int ct = blockIdx.x % a.col_tiles, rest = blockIdx.x / a.col_tiles;
-  const int rt = rest % a.row_tiles, e = rest / a.row_tiles;
-  const int64_t r0 = (int64_t)rt * 128 + 8 * q, c0 = (int64_t)ct * 128 + 8 * l;
+  const unsigned ct = blockIdx.x % (unsigned)a.col_tiles, rest = blockIdx.x / (unsigned)a.col_tiles;
+  const unsigned rt = rest % (unsigned)a.row_tiles, e = rest / (unsigned)a.row_tiles;
+  const int64_t r0 = (int64_t)rt * 128 + S * q, c0 = (int64_t)ct * 128 + 8 * l;
   const int64_t Kp = (int64_t)a.col_tiles * 128, Rp = (int64_t)a.row_tiles * 128;
   const T* x = (const T*)a.x + e * a.x_step;
-  float v[8][8];
+  float v[S][8];
   unsigned keep = 0;               // bit i: row i is written
-  // rows without a branch between their loads
-  int64_t src[8];
+  int64_t src[S];                  // its row of x, -1: zeros
+  int m[S];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = r0 + i;
-    src[i] = -1;
-    if (r < a.R) {
-      int64_t m = r;
-      if (a.row_map) m = a.row_map[r];
-      if (!a.row_map || m >= -1) keep |= 1u << i;
-      if (m >= 0) {
-        if (a.row_map) m = a.map_div ? m / a.map_div : r;
-        if (m < a.x_rows) src[i] = m;
-      }
-    }
+  for (int i = 0; i < S; ++i) m[i] = (int)(r0 + i);
+  if (a.row_map) {                 // loads without a branch between them
+#pragma unroll
+    for (int i = 0; i < S; ++i) m[i] = a.row_map[min(r0 + i, a.R - 1)];
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < S; ++i) {
+    src[i] = -1;
+    if (r0 + i >= a.R) continue;
+    if (!a.row_map || m[i] >= -1) keep |= 1u << i;
+    if (m[i] < 0) continue;
+    int64_t at = m[i];
+    if (a.row_map) at = a.map_div ? (int64_t)((unsigned)m[i] / (unsigned)a.map_div) : r0 + i;
+    if (at < a.x_rows) src[i] = at;
+  }
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
     if (src[i] >= 0) load8<DT>(x + src[i] * a.ldx, c0, a.K, v[i]);
   }
   if (GATED) {
+    float u[S][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float u[8];
+    for (int i = 0; i < S; ++i) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] = 0.0f;
-      if (src[i] >= 0) load8<DT>(x + src[i] * a.ldx + a.K, c0, a.K, u);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = silu(v[i][j]) * u[j];
+      for (int j = 0; j < 8; ++j) u[i][j] = 0.0f;
+      if (src[i] >= 0) load8<DT>(x + src[i] * a.ldx + a.K, c0, a.K, u[i]);
     }
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = silu(v[i][j]) * u[i][j];
   }
+  // the words of the transposed codes to their rows
+  const auto store_t = [&](uint8_t* to) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 128 * 8 / Q_THREADS; ++i) {
+      const int at = i * Q_THREADS + tid, c = at >> 3, p = at & 7;
+      const int64_t col = (int64_t)ct * 128 + c;
+      if (col < a.K)
+        *(i32x4_t*)(to + col * Rp + (int64_t)rt * 128 + 16 * p) = *(const i32x4_t*)(tile + tile_word(c, 4 * p));
+    }
+  };
   if (MODE & Q_ROWS) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t m = 0;
+    for (int i = 0; i < S; ++i) {
+      uint32_t mx = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[i][j]));
-      const GroupScale s = group_scale(row16_max(m));
+      for (int j = 0; j < 8; ++j) mx = max(mx, abs_bits(v[i][j]));
+      const GroupScale s = group_scale(row16_max(mx));
       if (!((keep >> i) & 1)) continue;
       const uint2 w = {codes4(v[i][0], v[i][1], v[i][2], v[i][3], s.inv),
                        codes4(v[i][4], v[i][5], v[i][6], v[i][7], s.inv)};
@@ -86,44 +109,47 @@ quant_kernel(QuantArgs a) {
   }
   if (MODE & Q_COLS) {
     if (a.row_map && !__syncthreads_or(keep != 0)) return;      // nothing but rows behind the last segment
-    uint32_t m[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      m[j] = 0;
+      uint32_t mx = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m[j] = max(m[j], abs_bits(v[i][j]));
-      m[j] = max(m[j], (uint32_t)__shfl_xor((int)m[j], 16, 64));
-      m[j] = max(m[j], (uint32_t)__shfl_xor((int)m[j], 32, 64));
-      if ((tid & 63) < 16) part[wave][8 * l + j] = m[j];
+      for (int i = 0; i < S; ++i) mx = max(mx, abs_bits(v[i][j]));
+      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16, 64));
+      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32, 64));
+      if ((tid & 63) < 16) part[wave][8 * l + j] = mx;
     }
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int c = 8 * l + j;
-      const GroupScale s = group_scale(max(max(part[0][c], part[1][c]), max(part[2][c], part[3][c])));
-      if (c0 + j >= a.K) continue;
-      const uint2 w = {codes4(v[0][j], v[1][j], v[2][j], v[3][j], s.inv),
-                       codes4(v[4][j], v[5][j], v[6][j], v[7][j], s.inv)};
-      *(uint2*)(a.codes_t + (c0 + j) * Rp + r0) = w;
-      if (q == 0) a.scales_t[(int64_t)rt * a.K + c0 + j] = s.scale;
+      uint32_t mx = 0;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) mx = max(mx, part[w][c]);
+      const GroupScale s = group_scale(mx);
+      tile[tile_word(c, q)] = codes4(v[0][j], v[1][j], v[2][j], v[3][j], s.inv);
+      if (q == 0 && c0 + j < a.K) a.scales_t[(int64_t)rt * a.K + c0 + j] = s.scale;
     }
+    store_t(a.codes_t);
   }
   if (MODE & Q_BLOCKS) {
-    uint32_t m = 0;
+    uint32_t mx = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < S; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[i][j]));
-    m = row16_max(m);
-    m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-    m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
-    if ((tid & 63) == 0) part[wave][0] = m;
+      for (int j = 0; j < 8; ++j) mx = max(mx, abs_bits(v[i][j]));
+    mx = row16_max(mx);
+    mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16, 64));
+    mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32, 64));
+    if ((tid & 63) == 0) part[wave][0] = mx;
     __syncthreads();
-    const GroupScale s = group_scale(max(max(part[0][0], part[1][0]), max(part[2][0], part[3][0])));
+    mx = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) mx = max(mx, part[w][0]);
+    const GroupScale s = group_scale(mx);
     const int64_t blocks = (int64_t)a.row_tiles * a.col_tiles;
     if (a.codes) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < S; ++i) {
         if (r0 + i >= a.R) continue;
         const uint2 w = {codes4(v[i][0], v[i][1], v[i][2], v[i][3], s.inv),
                          codes4(v[i][4], v[i][5], v[i][6], v[i][7], s.inv)};
@@ -133,13 +159,9 @@ quant_kernel(QuantArgs a) {
     }
     if (a.codes_t) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (c0 + j >= a.K) continue;
-        const uint2 w = {codes4(v[0][j], v[1][j], v[2][j], v[3][j], s.inv),
-                         codes4(v[4][j], v[5][j], v[6][j], v[7][j], s.inv)};
-        *(uint2*)(a.codes_t + ((int64_t)e * a.K + c0 + j) * Rp + r0) = w;
-      }
+      for (int j = 0; j < 8; ++j) tile[tile_word(8 * l + j, q)] = codes4(v[0][j], v[1][j], v[2][j], v[3][j], s.inv);
       if (tid == 0) a.scales_t[e * blocks + (int64_t)ct * a.row_tiles + rt] = s.scale;
+      store_t(a.codes_t + (int64_t)e * a.K * Rp);
     }
   }
 }
@@ -170,15 +192,16 @@ gated_backward_kernel(const typename Elem<DT>::type* __restrict__ z, int64_t ldz
 template <int MODE, bool GATED>
 int launch_quant(int dt, const QuantArgs& a, int64_t matrices, hipStream_t s) {
   const int64_t blocks = (int64_t)a.row_tiles * a.col_tiles * matrices;
-  if (dt == MOE_T_BF16) quant_kernel<MOE_T_BF16, MODE, GATED><<<(unsigned)blocks, 256, 0, s>>>(a);
-  else if (dt == MOE_T_F16) quant_kernel<MOE_T_F16, MODE, GATED><<<(unsigned)blocks, 256, 0, s>>>(a);
-  else quant_kernel<MOE_T_F32, MODE, GATED><<<(unsigned)blocks, 256, 0, s>>>(a);
+  if (dt == MOE_T_BF16) quant_kernel<MOE_T_BF16, MODE, GATED><<<(unsigned)blocks, Q_THREADS, 0, s>>>(a);
+  else if (dt == MOE_T_F16) quant_kernel<MOE_T_F16, MODE, GATED><<<(unsigned)blocks, Q_THREADS, 0, s>>>(a);
+  else quant_kernel<MOE_T_F32, MODE, GATED><<<(unsigned)blocks, Q_THREADS, 0, s>>>(a);
   return launched();
 }
 
 int64_t pad128(int64_t n) { return (n + 127) / 128 * 128; }
 
 constexpr int64_t MAX_SIZE = 1 << 30;
+constexpr int64_t MAX_TILES = MAX_BLOCKS / 2;      // of 512 threads
 
 }  // namespace
 
@@ -205,7 +228,7 @@ int moe_fp8_quantize(int dtype, const void* x, int64_t ldx, int64_t x_rows, cons
   const int64_t Kp = pad128(cols), Rp = pad128(rows);
   QuantArgs a{x, ldx, x_rows, 0, row_map, row_map ? (int)map_div : 1, rows, cols, codes, scales, codes_t, scales_t,
               (int)(Rp / 128), (int)(Kp / 128)};
-  if ((int64_t)a.row_tiles * a.col_tiles > MAX_BLOCKS) return bad(MOE_E_UNSUPPORTED, "too many values");
+  if ((int64_t)a.row_tiles * a.col_tiles > MAX_TILES) return bad(MOE_E_UNSUPPORTED, "too many values");
   if (outputs_shared({span(codes, rows * Kp), span(scales, Kp / 128 * rows * 4), span(codes_t, cols * Rp),
                       span(scales_t, Rp / 128 * cols * 4)},
                      {row_span(x, x_rows, width, ldx, b), span(row_map, rows * 4)}))
@@ -228,7 +251,7 @@ int moe_fp8_quantize_weights(int dtype, const void* w, int64_t E, int64_t N, int
   if (!w) return bad(MOE_E_INVAL, "null argument");
   if (((uintptr_t)codes | (uintptr_t)codes_t) % 16) return bad(MOE_E_INVAL, "codes start on 16 bytes");
   const int64_t Kp = pad128(K), Np = pad128(N), blocks = Np / 128 * (Kp / 128);
-  if (blocks > MAX_BLOCKS || blocks * E > MAX_BLOCKS) return bad(MOE_E_UNSUPPORTED, "too many values");
+  if (blocks > MAX_TILES || blocks * E > MAX_TILES) return bad(MOE_E_UNSUPPORTED, "too many values");
   if (outputs_shared({span(codes, E * N * Kp), span(scales, E * blocks * 4), span(codes_t, E * K * Np),
                       span(scales_t, E * blocks * 4)},
                      {span(w, E * N * K * b)}))

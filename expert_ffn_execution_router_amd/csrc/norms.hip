@@ -20,7 +20,7 @@
 
 namespace {
 
-constexpr int MAX_COLS = 16384;
+constexpr int MAX_COLS = 16384, MAX_BWD_COLS = 8192;
 
 struct NormArgs {
   const void* y;
@@ -71,10 +71,21 @@ struct NormBwdArgs {
   bool w_f32, gate_f32, dgate_f32;
 };
 
+// Sum over the wave, in all of its lanes: inside rows of 16 lanes, then over
+// the rows; lane 63 has it.  (Exchanges through LDS, 36 for six sums, were a
+// third of the backward pass.)
+DEV float wave_total(float v) {
+#define STEP(CTRL, ROWS) \
+  v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, false));
+  STEP(0x111, 0xf) STEP(0x112, 0xf) STEP(0x114, 0xf) STEP(0x118, 0xf) STEP(0x142, 0xa) STEP(0x143, 0xc)
+#undef STEP
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+
 // Sum over the threads of a row: one wave, or all waves of the workgroup.
 template <int TPR>
 DEV float row_sum(float v, float* lds) {
-  v = wave_sum(v);
+  v = wave_total(v);
   if (TPR == 64) return v;
   __syncthreads();                               // lds is free again
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
@@ -85,14 +96,69 @@ DEV float row_sum(float v, float* lds) {
   return s;
 }
 
+// N such sums at once.
+template <int TPR, int N>
+DEV void row_sums(float (&v)[N], float (*lds)[16]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = wave_total(v[k]);
+  if (TPR == 64) return;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0)
+#pragma unroll
+    for (int k = 0; k < N; ++k) lds[k][threadIdx.x >> 6] = v[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    v[k] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < TPR / 64; ++i) v[k] += lds[k][i];
+  }
+}
+
+// Columns c .. c+7 of a row, zeros from cols on.  EVEN (cols a multiple of 8):
+// without a branch, so that a row's loads are in flight together.
+template <int DT, bool EVEN>
+DEV void load_row(const typename Elem<DT>::type* row, long c, long cols, float (&f)[8]) {
+  if (!EVEN) return load8<DT>(row, c, cols, f);
+  load_vals<DT, 8>(row + min(c, cols - 8), f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = c < cols ? f[i] : 0.0f;
+}
+
+// The same, as they are stored.
 template <int DT>
+using Raw = Pack<typename Elem<DT>::type, 8>;
+
+template <int DT, bool EVEN>
+DEV Raw<DT> load_raw(const typename Elem<DT>::type* row, long c, long cols) {
+  Raw<DT> r = {};
+  if (EVEN) {
+    __builtin_memcpy(&r, row + min(c, cols - 8), sizeof(r));
+    if (c >= cols) r = Raw<DT>{};
+  } else if (c + 8 <= cols) {
+    __builtin_memcpy(&r, row + c, sizeof(r));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < cols) r.v[i] = row[c + i];
+  }
+  return r;
+}
+
+template <int DT>
+DEV void values(const Raw<DT>& r, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = Elem<DT>::load(r.v[i]);
+}
+
+template <int DT, bool EVEN>
 DEV void load_param(const void* p, bool f32, long c, long cols, float (&f)[8]) {
-  if (DT == MOE_T_F32 || f32) load8<MOE_T_F32>((const float*)p, c, cols, f);
-  else load8<DT>((const typename Elem<DT>::type*)p, c, cols, f);
+  if (DT == MOE_T_F32 || f32) load_row<MOE_T_F32, EVEN>((const float*)p, c, cols, f);
+  else load_row<DT, EVEN>((const typename Elem<DT>::type*)p, c, cols, f);
 }
 
 // The gate of row t, columns c .. c+7 (zeros past cols).
-template <int DT>
+template <int DT, bool EVEN>
 DEV void load_gate(const void* p, bool f32, int64_t t, int64_t gr, int64_t gc, long c, long cols, float (&f)[8]) {
   typedef typename Elem<DT>::type T;
   if (gc == 0) {
@@ -100,13 +166,13 @@ DEV void load_gate(const void* p, bool f32, int64_t t, int64_t gr, int64_t gc, l
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = g;
   } else if (DT == MOE_T_F32 || f32) {
-    load8<MOE_T_F32>((const float*)p + t * gr, c, cols, f);
+    load_row<MOE_T_F32, EVEN>((const float*)p + t * gr, c, cols, f);
   } else {
-    load8<DT>((const T*)p + t * gr, c, cols, f);
+    load_row<DT, EVEN>((const T*)p + t * gr, c, cols, f);
   }
 }
 
-template <int DT, int RT, int TPR, int NV>
+template <int DT, int RT, int TPR, int NV, bool EVEN>
 __global__ void __launch_bounds__(TPR == 64 ? 256 : TPR)
 norm_kernel(NormArgs a) {
   typedef typename Elem<DT>::type TD;
@@ -120,7 +186,7 @@ norm_kernel(NormArgs a) {
   float h[NV][8];
   if (a.r) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) load8<RT>((const TR*)a.r + t * a.ldr, (u0 + i * TPR) * 8, cols, h[i]);
+    for (int i = 0; i < NV; ++i) load_row<RT, EVEN>((const TR*)a.r + t * a.ldr, (u0 + i * TPR) * 8, cols, h[i]);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -134,7 +200,7 @@ norm_kernel(NormArgs a) {
   if (a.y) {
     float y[NV][8];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) load8<DT>((const TD*)a.y + t * a.ldy, (u0 + i * TPR) * 8, cols, y[i]);
+    for (int i = 0; i < NV; ++i) load_row<DT, EVEN>((const TD*)a.y + t * a.ldy, (u0 + i * TPR) * 8, cols, y[i]);
     float rs = 1.0f;
     if (a.w) {
       float s = 0.0f;
@@ -149,13 +215,13 @@ norm_kernel(NormArgs a) {
       const long c = (u0 + i * TPR) * 8;
       if (a.w) {
         float w[8];
-        load_param<DT>(a.w, a.w_f32, c, cols, w);
+        load_param<DT, EVEN>(a.w, a.w_f32, c, cols, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[i][j] = y[i][j] * rs * w[j];
       }
       if (a.gate) {
         float g[8];
-        load_gate<DT>(a.gate, a.gate_f32, t, a.gr, a.gc, c, cols, g);
+        load_gate<DT, EVEN>(a.gate, a.gate_f32, t, a.gr, a.gc, c, cols, g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[i][j] *= g[j];
       }
@@ -183,7 +249,7 @@ norm_kernel(NormArgs a) {
   for (int i = 0; i < NV; ++i) {
     const long c = (u0 + i * TPR) * 8;
     float w[8];
-    load_param<DT>(a.w2, a.w_f32, c, cols, w);
+    load_param<DT, EVEN>(a.w2, a.w_f32, c, cols, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) h[i][j] = c + j < cols ? h[i][j] * rs * w[j] : 0.0f;
     if (!a.scales) {
@@ -202,128 +268,212 @@ norm_kernel(NormArgs a) {
   }
 }
 
-template <int DT, int RT, int TPR, int NV>
+// With D = dn w', G = gate w and m = mean(D n): <d, G y> = <dh, G y> + (<D, G y>
+// - m <h, G y> / rms(h)) / rms(h), so that one joint sum over the row, of values
+// as they were read, gives both roots and both means.  HELD units of a thread
+// stay in registers between that sum and the results; 0 (the widest rows):
+// they are read again, and the column sums are kept in LDS, as neither fits
+// without spilling registers.
+template <int DT, int RT, int TPR, int HELD, bool EVEN>
 __global__ void __launch_bounds__(TPR == 64 ? 256 : TPR)
 norm_bwd_kernel(NormBwdArgs a) {
   typedef typename Elem<DT>::type TD;
   typedef typename Elem<RT>::type TR;
-  __shared__ float lds[16];
+  constexpr bool WIDE = HELD == 0, AHEAD = HELD == 1;
+  constexpr int NV = WIDE ? 1 : HELD;
+  __shared__ float lds[6][16];
+  extern __shared__ __align__(16) float lds_sums[];     // WIDE: [3][MAX_BWD_COLS]
   const int u0 = TPR == 64 ? threadIdx.x & 63 : threadIdx.x;
   const int part = TPR == 64 ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
-  const int cols = a.cols;
+  const int cols = a.cols, units = WIDE ? (cols + 8 * TPR - 1) / (8 * TPR) : NV;
   const float inv_n = 1.0f / (float)cols;
-  float sw[NV][8] = {}, sw2[NV][8] = {}, sg[NV][8] = {};
-  for (int64_t t = part; t < a.T; t += a.parts) {
-    float d[NV][8];
+  const auto column = [&](int i) { return (long)(u0 + i * TPR) * 8; };
+  const auto each = [&](auto f) __attribute__((always_inline)) {
+    if constexpr (WIDE) {
+#pragma unroll 1
+      for (int i = 0; i < units; ++i) f(i);
+    } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (a.dh) load8<RT>((const TR*)a.dh + t * a.lddh, (u0 + i * TPR) * 8, cols, d[i]);
-      else
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[i][j] = 0.0f;
+      for (int i = 0; i < NV; ++i) f(i);
     }
+  };
+  // column sums of the thread's units: dw, dw', dgate
+  float sums[3][NV][8] = {};
+  const auto count = [&](int k, int i, const float (&v)[8]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (WIDE) lds_sums[k * MAX_BWD_COLS + column(i) + j] += v[j];
+      else sums[k][i][j] += v[j];
+    }
+  };
+  if (WIDE)
+    each([&](int i) {
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) lds_sums[k * MAX_BWD_COLS + column(i) + j] = 0.0f;
+    });
+  struct Unit {
+    Raw<RT> d, n;                                       // dh, h
+    Raw<DT> g, x;                                       // dn, y
+    float k[8];                                         // gate
+  };
+  const bool row_gate = a.gate && (a.gr || !AHEAD);     // its gate comes with a row
+  const auto read = [&](int64_t t, int i, Unit& u) __attribute__((always_inline)) {
+    const long c = column(i);
+    u.d = u.n = Raw<RT>{};
+    u.g = u.x = Raw<DT>{};
+    if (a.dh) u.d = load_raw<RT, EVEN>((const TR*)a.dh + t * a.lddh, c, cols);
     if (a.dn) {
-      float n[NV][8], g[NV][8], s = 0.0f;
+      u.n = load_raw<RT, EVEN>((const TR*)a.h + t * a.ldh, c, cols);
+      u.g = load_raw<DT, EVEN>((const TD*)a.dn + t * a.lddn, c, cols);
+    }
+    if (a.y) u.x = load_raw<DT, EVEN>((const TD*)a.y + t * a.ldy, c, cols);
+    if (row_gate) load_gate<DT, EVEN>(a.gate, a.gate_f32, t, a.gr, a.gc, c, cols, u.k);
+  };
+  // AHEAD: the next row is on its way while one is worked on (a CU holds one
+  // workgroup of 512), and what is the same for every row stays in registers,
+  // as its loads would wait for that row.  4099 rows of 4096 bf16 with a gate
+  // per column: 58 us (201 MB, 3.5 TB/s); 96 without, 82 without the second.
+  float hw[NV][8], hf[NV][8], hk[NV][8];                // w, w', gate
+  const auto weights = [&](int i, float (&w)[8], float (&f)[8]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = f[j] = 1.0f;
+    if (a.dn) load_param<DT, EVEN>(a.w2, a.w_f32, column(i), cols, f);
+    if (a.w) load_param<DT, EVEN>(a.w, a.w_f32, column(i), cols, w);
+  };
+  Unit next[NV], cur[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) hk[i][j] = next[i].k[j] = cur[i].k[j] = 1.0f;
+    if (!AHEAD) continue;
+    weights(i, hw[i], hf[i]);
+    if (a.gate && !row_gate) load_gate<DT, EVEN>(a.gate, a.gate_f32, 0, a.gr, a.gc, column(i), cols, hk[i]);
+    if (part < a.T) read(part, i, next[i]);
+  }
+  for (int64_t t = part; t < a.T; t += a.parts) {
+    if (AHEAD) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        load8<RT>((const TR*)a.h + t * a.ldh, (u0 + i * TPR) * 8, cols, n[i]);
-        load8<DT>((const TD*)a.dn + t * a.lddn, (u0 + i * TPR) * 8, cols, g[i]);
+        cur[i] = next[i];
+        if (!row_gate)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s += n[i][j] * n[i][j];
+          for (int j = 0; j < 8; ++j) cur[i].k[j] = hk[i][j];
+        if (t + a.parts < a.T) read(t + a.parts, i, next[i]);
       }
-      const float rs = 1.0f / sqrtf(row_sum<TPR>(s, lds) * inv_n + a.eps2);
-      s = 0.0f;
+    } else if (!WIDE) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float w[8];
-        load_param<DT>(a.w2, a.w_f32, (u0 + i * TPR) * 8, cols, w);
+      for (int i = 0; i < NV; ++i) read(t, i, cur[i]);
+    }
+    struct Values {
+      float d[8], n[8], g[8], x[8], w[8], f[8], k[8];
+    };
+    const auto get = [&](int i, Values& v) __attribute__((always_inline)) {
+      if (WIDE) read(t, i, cur[0]);
+      const Unit& u = cur[WIDE ? 0 : i];
+      values<RT>(u.d, v.d);
+      values<RT>(u.n, v.n);
+      values<DT>(u.g, v.g);
+      values<DT>(u.x, v.x);
+      if (!AHEAD) weights(i, v.w, v.f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (AHEAD) {
+          v.w[j] = hw[WIDE ? 0 : i][j];
+          v.f[j] = hf[WIDE ? 0 : i][j];
+        }
+        v.k[j] = a.gate && column(i) + j < cols ? u.k[j] : 1.0f;
+      }
+    };
+    // h^2, D h, y^2, dh G y, D G y, h G y
+    float s[6] = {};
+    each([&](int i) __attribute__((always_inline)) {
+      Values v;
+      get(i, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float D = v.g[j] * v.f[j], gy = v.x[j] * (v.w[j] * v.k[j]);
+        s[0] += v.n[j] * v.n[j];
+        s[1] += D * v.n[j];
+        s[2] += v.x[j] * v.x[j];
+        s[3] += v.d[j] * gy;
+        s[4] += D * gy;
+        s[5] += v.n[j] * gy;
+      }
+    });
+    row_sums<TPR>(s, lds);
+    const float rh = a.dn ? 1.0f / sqrtf(s[0] * inv_n + a.eps2) : 0.0f, m = rh * s[1] * inv_n;
+    const float ry = a.w ? 1.0f / sqrtf(s[2] * inv_n + a.eps) : 1.0f;
+    const float mean = a.w ? ry * (s[3] + rh * (s[4] - m * rh * s[5])) * inv_n : 0.0f;      // <d, G x>
+    const bool row_sum_of_gate = a.dgate && !a.dgc;     // a gate per row: <d, w x>
+    float dg[1] = {0.0f};
+    each([&](int i) __attribute__((always_inline)) {
+      const long c = column(i);
+      Values v;
+      get(i, v);
+      float out[8];
+      if (a.dn) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          n[i][j] *= rs;
-          sw2[i][j] += g[i][j] * n[i][j];
-          g[i][j] *= w[j];
-          s += g[i][j] * n[i][j];
+          const float n = v.n[j] * rh;
+          out[j] = v.g[j] * n;
+          v.d[j] += rh * (v.g[j] * v.f[j] - n * m);
         }
+        if (a.set_w2 >= 0) count(1, i, out);
       }
-      const float mean = row_sum<TPR>(s, lds) * inv_n;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[i][j] += rs * (g[i][j] - n[i][j] * mean);
-    }
-    if (a.y) {
-      float x[NV][8], dv[NV][8], rs = 1.0f, s = 0.0f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        load8<DT>((const TD*)a.y + t * a.ldy, (u0 + i * TPR) * 8, cols, x[i]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s += x[i][j] * x[i][j];
-      }
-      if (a.w) rs = 1.0f / sqrtf(row_sum<TPR>(s, lds) * inv_n + a.eps);
-      float mean = 0.0f, dg = 0.0f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const long c = (u0 + i * TPR) * 8;
-        float w[8], g[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = g[j] = 1.0f;
-        if (a.w) load_param<DT>(a.w, a.w_f32, c, cols, w);
-        if (a.gate) load_gate<DT>(a.gate, a.gate_f32, t, a.gr, a.gc, c, cols, g);
-        float full[8];
+      if (a.y) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          x[i][j] *= rs;
-          const float e = d[i][j] * x[i][j];
-          full[j] = e * w[j];
-          dg += full[j];
-          sg[i][j] += full[j];
-          sw[i][j] += e * g[j];
-          dv[i][j] = d[i][j] * g[j] * w[j];
-          mean += dv[i][j] * x[i][j];
+          v.x[j] *= ry;
+          out[j] = v.d[j] * v.x[j] * v.k[j];
         }
-        if (a.dgate && a.dgc && c < cols) {           // a value of its own for each of the row
-          if (DT == MOE_T_F32 || a.dgate_f32) store8<MOE_T_F32>((float*)a.dgate + t * a.dgr, c, cols, full);
-          else store8<DT>((TD*)a.dgate + t * a.dgr, c, cols, full);
+        if (a.set_w >= 0) count(0, i, out);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          out[j] = v.d[j] * v.x[j] * v.w[j];
+          dg[0] += out[j];
         }
-      }
-      mean = a.w ? row_sum<TPR>(mean, lds) * inv_n : 0.0f;
-      if (a.dgate && !a.dgc) {
-        dg = row_sum<TPR>(dg, lds);
-        if (u0 == 0) {
-          if (DT == MOE_T_F32 || a.dgate_f32) ((float*)a.dgate)[t * a.dgr] = dg;
-          else ((TD*)a.dgate)[t * a.dgr] = Elem<DT>::store(dg);
+        if (a.set_g >= 0) count(2, i, out);
+        if (a.dgate && a.dgc && c < cols) {             // a value of its own for each of the row
+          if (DT == MOE_T_F32 || a.dgate_f32) store8<MOE_T_F32>((float*)a.dgate + t * a.dgr, c, cols, out);
+          else store8<DT>((TD*)a.dgate + t * a.dgr, c, cols, out);
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) out[j] = ry * (v.d[j] * v.k[j] * v.w[j] - v.x[j] * mean);
+        if (c < cols) store8<DT>((TD*)a.dy + t * a.lddy, c, cols, out);
       }
+      if (a.dr && c < cols) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const long c = (u0 + i * TPR) * 8;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dv[i][j] = rs * (dv[i][j] - x[i][j] * mean);
-        if (c < cols) store8<DT>((TD*)a.dy + t * a.lddy, c, cols, dv[i]);
+        for (int j = 0; j < 8; ++j) out[j] = v.d[j] * a.alpha;
+        store8<RT>((TR*)a.dr + t * a.lddr, c, cols, out);
       }
-    }
-    if (a.dr) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const long c = (u0 + i * TPR) * 8;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[i][j] *= a.alpha;
-        if (c < cols) store8<RT>((TR*)a.dr + t * a.lddr, c, cols, d[i]);
+    });
+    if (row_sum_of_gate) {
+      row_sums<TPR>(dg, lds);
+      if (u0 == 0) {
+        if (DT == MOE_T_F32 || a.dgate_f32) ((float*)a.dgate)[t * a.dgr] = dg[0];
+        else ((TD*)a.dgate)[t * a.dgr] = Elem<DT>::store(dg[0]);
       }
     }
   }
   if (part >= a.parts) return;
+  each([&](int i) __attribute__((always_inline)) {
+    const long c = column(i);
+    if (c >= cols) return;
+    const int set[3] = {a.set_w, a.set_w2, a.set_g};
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const long c = (u0 + i * TPR) * 8;
-    if (c >= cols) continue;
-    const auto put = [&](int set, const float (&v)[8]) {
-      if (set >= 0) store8<MOE_T_F32>(a.part + ((int64_t)set * a.parts + part) * cols, c, cols, v);
-    };
-    put(a.set_w, sw[i]);
-    put(a.set_w2, sw2[i]);
-    put(a.set_g, sg[i]);
-  }
+    for (int k = 0; k < 3; ++k) {
+      if (set[k] < 0) continue;
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (WIDE) v[j] = lds_sums[k * MAX_BWD_COLS + c + j];
+        else v[j] = sums[k][i][j];
+      }
+      store8<MOE_T_F32>(a.part + ((int64_t)set[k] * a.parts + part) * cols, c, cols, v);
+    }
+  });
 }
 
 // Column sums over the parts: 64 columns to a workgroup, its 16 waves every
@@ -381,10 +531,21 @@ int by_types(int dt, int rt, F f) {
   return dt == MOE_T_BF16 ? f(BF(), BF()) : f(HF(), HF());
 }
 
+// The same for the backward pass (threads of a row, units held).
+template <typename F>
+int by_bwd_width(int64_t cols, F f) {
+  typedef std::integral_constant<int, 1> One;
+  if (cols <= 512) return f(std::integral_constant<int, 64>(), One());
+  if (cols <= 1024) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
+  if (cols <= 2048) return f(std::integral_constant<int, 256>(), One());
+  if (cols <= 4096) return f(std::integral_constant<int, 512>(), One());
+  return f(std::integral_constant<int, 512>(), std::integral_constant<int, 0>());
+}
+
 // Rows the workgroups of the backward pass take in turn, and the waves or
 // workgroups whose column sums are joined.
 int64_t bwd_parts(int64_t T, int64_t cols) {
-  const int64_t at_once = cols <= 1024 ? 4096 : cols <= 4096 ? 1024 : 512;
+  const int64_t at_once = cols <= 1024 ? 2048 : cols <= 2048 ? 512 : 256;
   return std::max<int64_t>(std::min(T, at_once), 1);
 }
 
@@ -455,15 +616,18 @@ int moe_norm(int dtype, const void* y, int64_t ldy, int rtype, const void* resid
   return by_types(dtype, rtype, [&](auto d, auto r) {
     return by_width(cols, [&](auto tpr, auto nv) {
       const int64_t blocks = tpr.value == 64 ? (T + 3) / 4 : T;
-      norm_kernel<d.value, r.value, tpr.value, nv.value>
-          <<<(unsigned)blocks, tpr.value == 64 ? 256 : tpr.value, 0, (hipStream_t)stream>>>(a);
+      const unsigned threads = tpr.value == 64 ? 256 : tpr.value;
+      if (cols % 8 == 0)
+        norm_kernel<d.value, r.value, tpr.value, nv.value, true><<<(unsigned)blocks, threads, 0, (hipStream_t)stream>>>(a);
+      else
+        norm_kernel<d.value, r.value, tpr.value, nv.value, false><<<(unsigned)blocks, threads, 0, (hipStream_t)stream>>>(a);
       return launched();
     });
   });
 }
 
 size_t moe_norm_backward_workspace_bytes(int64_t T, int64_t cols) {
-  if (T < 0 || T > I32_MAX || cols < 1 || cols > MAX_COLS) return 0;
+  if (T < 0 || T > I32_MAX || cols < 1 || cols > MAX_BWD_COLS) return 0;
   return (size_t)(3 * bwd_parts(T, cols) * cols * 4);
 }
 
@@ -475,6 +639,7 @@ int moe_norm_backward(int dtype, int rtype, const void* dh, int64_t lddh, const 
                       float next_eps, void* ws, size_t ws_bytes, void* stream) {
   int rc = check_types(dtype, rtype, wtype, gate != nullptr, gtype);
   if (rc || (rc = check_size(T, cols))) return rc;
+  if (cols > MAX_BWD_COLS) return bad(MOE_E_UNSUPPORTED, "gradients of rows wider than 8192");
   const int b = elem_bytes(dtype), br = elem_bytes(rtype), bw = elem_bytes(wtype), bg = gate ? elem_bytes(gtype) : 0;
   if ((dh && lddh < cols) || (y && ldy < cols) || (dnext && lddn < cols) || (dnext && ldh < cols) ||
       (dy && lddy < cols) || (dr && lddr < cols))
@@ -522,11 +687,20 @@ int moe_norm_backward(int dtype, int rtype, const void* dh, int64_t lddh, const 
                       dgtype == MOE_T_F32};
   const hipStream_t s = (hipStream_t)stream;
   rc = by_types(dtype, rtype, [&](auto d, auto r) {
-    return by_width(cols, [&](auto tpr, auto nv) {
+    return by_bwd_width(cols, [&](auto tpr, auto nv) {
       const int64_t blocks = tpr.value == 64 ? (parts + 3) / 4 : parts;
-      norm_bwd_kernel<d.value, r.value, tpr.value, nv.value>
-          <<<(unsigned)blocks, tpr.value == 64 ? 256 : tpr.value, 0, s>>>(a);
-      return launched();
+      const unsigned threads = tpr.value == 64 ? 256 : tpr.value;
+      constexpr int LDS = nv.value == 0 ? 3 * MAX_BWD_COLS * 4 : 0;
+      const auto go = [&](auto kernel) {
+        if (LDS) {
+          const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
+          if (e != hipSuccess) return bad(MOE_E_HIP, hipGetErrorString(e));
+        }
+        kernel<<<(unsigned)blocks, threads, LDS, s>>>(a);
+        return launched();
+      };
+      return cols % 8 == 0 ? go(norm_bwd_kernel<d.value, r.value, tpr.value, nv.value, true>)
+                           : go(norm_bwd_kernel<d.value, r.value, tpr.value, nv.value, false>);
     });
   });
   if (rc || !sets) return rc;

@@ -48,12 +48,12 @@ def padded(n: int) -> int:
 
 
 def _pair(name, codes, scales, dev, cshape, sshape):
-    """Addresses of codes and their scales, or two Nones."""
-    if codes is None and scales is None:
-        return None, None
+    """Addresses of codes and their scales."""
     if codes is None or scales is None:
+        if codes is None and scales is None:
+            return None, None
         raise ValueError(f"{name}: codes and scales come together")
-    return (A.whole(name, codes, dev, F8, cshape), A.whole(name.replace("codes", "scales"), scales, dev, _F32, sshape))
+    return A.whole(name, codes, dev, F8, cshape), A.whole(f"scales of {name}", scales, dev, _F32, sshape)
 
 
 def quantize(x, codes=None, scales=None, codes_t=None, scales_t=None, row_map=None, map_div=1, gated=False,
@@ -115,8 +115,8 @@ def _matmul(a, a_scales, offsets, w, w_scales, out, counts, E, stream):
     if K % 128:
         raise ValueError(f"a: {K} columns, expected whole groups of 128")
     G = K // 128
-    ap, asp = _pair("codes of a", a, a_scales, dev, (n, K), (G, n))
-    wp, wsp = _pair("codes of w", w, w_scales, dev, (*lead, N, K), (*lead, padded(N) // 128, G))
+    ap, asp = _pair("a", a, a_scales, dev, (n, K), (G, n))
+    wp, wsp = _pair("w", w, w_scales, dev, (*lead, N, K), (*lead, padded(N) // 128, G))
     ot, op, ldo, _ = A.rows("out", out, dev, n, N)
     A.launch(B.lib().moe_fp8_matmul, dev, stream, ap, asp, offsets, counts, E, n, wp, wsp, N, K, ot, op, ldo)
 
@@ -168,8 +168,8 @@ def weight_gradient(dy_t, dy_scales, x_t, x_scales, dw, offsets=None, add=False,
     if rows % 128:
         raise ValueError(f"dy_t: {rows} rows, expected whole groups of 128")
     E = 1 if offsets is None else dw.shape[0]
-    dp, dsp = _pair("codes of dy", dy_t, dy_scales, dev, (N, rows), (rows // 128, N))
-    xp, xsp = _pair("codes of x", x_t, x_scales, dev, (K, rows), (rows // 128, K))
+    dp, dsp = _pair("dy_t", dy_t, dy_scales, dev, (N, rows), (rows // 128, N))
+    xp, xsp = _pair("x_t", x_t, x_scales, dev, (K, rows), (rows // 128, K))
     shape = (N, K) if offsets is None else (E, N, K)
     wp = A.whole("dw", dw, dev, _F32, shape)
     op = None if offsets is None else A.whole("offsets", offsets, dev, _I32, (E + 1,))
@@ -198,8 +198,8 @@ def layer(x, router, gate_up, gate_up_scales, down, down_scales, out, ids, weigh
     xt, xp, ldx, _ = A.rows("x", x, dev, T, H, _16)
     rp = A.whole("router", router, dev, _F32, (E, H))
     bp = None if bias is None else A.whole("bias", bias, dev, _F32, (E,))
-    gp, gs = _pair("codes of gate_up", gate_up, gate_up_scales, dev, (E, 2 * I, H), (E, I // 64, H // 128))
-    dp, ds = _pair("codes of down", down, down_scales, dev, (E, H, I), (E, H // 128, I // 128))
+    gp, gs = _pair("gate_up", gate_up, gate_up_scales, dev, (E, 2 * I, H), (E, I // 64, H // 128))
+    dp, ds = _pair("down", down, down_scales, dev, (E, H, I), (E, H // 128, I // 128))
     ot, op, ldo, _ = A.rows("out", out, dev, T, H)
     ap, ldb = None, 0
     if base is not None:

@@ -5,7 +5,8 @@ gate and residual scale, and their gradients:
     after    out  = alpha r + gate * (y / rms(y)) w
              next = (out / rms(out)) w2
 
-with rms(v) = sqrt(mean v^2 + eps) over a row of up to 16384 columns.  y (the
+with rms(v) = sqrt(mean v^2 + eps) over a row of up to 16384 columns (8192 for
+the gradients).  y (the
 block's result) and next have one type, the residual rows r and out that type
 or fp32; weights [cols] and the gate ([T, 1], [1, cols] or [T, cols]) y's type
 or fp32.  next may be e4m3 codes [T, padded(cols)] with scales
@@ -28,35 +29,45 @@ from . import _args as A
 from . import binding as B
 
 _F32, F8 = torch.float32, torch.float8_e4m3fn
+# types of what goes with rows of a type: that type or fp32
+_WITH = {dt: {dt: code, _F32: B.MOE_T_F32} for dt, code in A.TYPES.items()}
 
 
-def _params(dev, cols, dtype, **weights):
-    """Addresses of the weights, and their one type code."""
-    code, first, out = A.TYPES[dtype], None, []
-    for name, w in weights.items():
-        if w is None:
-            out.append(None)
-            continue
-        if w.dtype not in (dtype, _F32):
-            raise ValueError(f"{name}: type {w.dtype}, expected {dtype} or fp32")
-        if first is not None and w.dtype != first:
-            raise ValueError(f"{name}: type {w.dtype}, the other weight has {first}")
-        first, code = w.dtype, A.TYPES[w.dtype]
-        out.append(A.whole(name, w, dev, w.dtype, (cols,)))
-    return code, out
+def _weight(name, w, dev, cols, types):
+    """Type code and address of a weight."""
+    code = types.get(w.dtype)
+    if code is None:
+        raise ValueError(f"{name}: type {w.dtype} is not one of {[str(x) for x in types]}")
+    return code, A.whole(name, w, dev, w.dtype, (cols,))
 
 
-def _gate(name, g, dev, T, cols, dtype):
+def _weights(weight, next_weight, dev, cols, types):
+    """Their one type code and addresses (None: not there)."""
+    if weight is None:
+        if next_weight is None:
+            return B.MOE_T_F32, None, None
+        code, p = _weight("next_weight", next_weight, dev, cols, types)
+        return code, None, p
+    code, p = _weight("weight", weight, dev, cols, types)
+    if next_weight is None:
+        return code, p, None
+    other, q = _weight("next_weight", next_weight, dev, cols, types)
+    if other != code:
+        raise ValueError(f"next_weight: type {next_weight.dtype}, weight has {weight.dtype}")
+    return code, p, q
+
+
+def _gate(name, g, dev, T, cols, types):
     """Type code, address and strides (0 along a spread axis)."""
     if g is None:
-        return A.TYPES[dtype], None, 0, 0
-    if tuple(g.shape) not in ((T, 1), (1, cols), (T, cols)):
-        raise ValueError(f"{name}: shape {tuple(g.shape)}, expected [{T}, 1], [1, {cols}] or [{T}, {cols}]")
-    types = {dtype: A.TYPES[dtype], _F32: B.MOE_T_F32}
-    code, p, ld, _ = A.rows(name, g, dev, None, g.shape[1], types)
-    if tuple(g.shape) == (T, 1):
+        return B.MOE_T_F32, None, 0, 0
+    shape = tuple(g.shape)
+    if shape not in ((T, 1), (1, cols), (T, cols)):
+        raise ValueError(f"{name}: shape {shape}, expected [{T}, 1], [1, {cols}] or [{T}, {cols}]")
+    code, p, ld, _ = A.rows(name, g, dev, None, shape[1], types)
+    if shape == (T, 1):
         return code, p, ld, 0
-    return code, p, 0 if g.shape[0] == 1 else ld, 1
+    return code, p, 0 if shape[0] == 1 else ld, 1
 
 
 def _next(name, out, scales, dev, T, cols, dtype):
@@ -90,9 +101,11 @@ def before(x, weight, out, scales=None, eps=1e-6, stream=None):
     _block_type("x", x)
     # the block's type: that of the rows it reads
     dtype = out.dtype if out.dtype != F8 else weight.dtype if weight.dtype != _F32 else x.dtype
-    _block_type("out", out) if out.dtype != F8 else None
-    rt, xp, ldx, _ = A.rows("x", x, dev, T, cols, {dtype: A.TYPES.get(dtype), _F32: B.MOE_T_F32})
-    wt, (wp,) = _params(dev, cols, dtype, weight=weight)
+    if dtype not in _WITH:
+        raise ValueError(f"out: type {dtype} is not one of {[str(x) for x in A.TYPES]}")
+    types = _WITH[dtype]
+    rt, xp, ldx, _ = A.rows("x", x, dev, T, cols, types)
+    wt, wp = _weight("weight", weight, dev, cols, types)
     op, ldo, sp = _next("out", out, scales, dev, T, cols, dtype)
     A.launch(B.lib().moe_norm, dev, stream, A.TYPES[dtype], None, 0, rt, xp, ldx, 1.0, wt, None, wt, None, 0, 0, None,
              0, wp, op, ldo, sp, T, cols, eps, eps)
@@ -107,13 +120,13 @@ def after(y, residual, out, weight=None, gate=None, alpha=1.0, eps=1e-6, next_we
         raise ValueError(f"y: shape {tuple(y.shape)}, expected rows")
     dev, (T, cols), dtype = y.get_device(), y.shape, _block_type("y", y)
     dt, yp, ldy, _ = A.rows("y", y, dev, T, cols)
-    types = {dtype: dt, _F32: B.MOE_T_F32}
+    types = _WITH[dtype]
     rt, rp, ldr, _ = A.rows("residual", residual, dev, T, cols, types)
     ot, op, ldo, _ = A.rows("out", out, dev, T, cols, types)
     if ot != rt:
         raise ValueError(f"out: type {out.dtype}, the residual has {residual.dtype}")
-    wt, (wp, np_) = _params(dev, cols, dtype, weight=weight, next_weight=next_weight)
-    gt, gp, gr, gc = _gate("gate", gate, dev, T, cols, dtype)
+    wt, wp, np_ = _weights(weight, next_weight, dev, cols, types)
+    gt, gp, gr, gc = _gate("gate", gate, dev, T, cols, types)
     xp, ldx, sp = None, 0, None
     if next_out is not None:
         if next_weight is None:
@@ -146,7 +159,7 @@ def before_backward(dout, x, weight, dx, dweight=None, base=None, eps=1e-6, ws=N
         raise ValueError(f"x: shape {tuple(x.shape)}, expected rows")
     dev, (T, cols), dtype = x.get_device(), x.shape, _block_type("dout", dout)
     dt, gp, ldg, _ = A.rows("dout", dout, dev, T, cols)
-    types = {dtype: dt, _F32: B.MOE_T_F32}
+    types = _WITH[dtype]
     rt, xp, ldx, _ = A.rows("x", x, dev, T, cols, types)
     ot, op, ldo, _ = A.rows("dx", dx, dev, T, cols, types)
     bt, bp, ldb = rt, None, 0
@@ -154,7 +167,7 @@ def before_backward(dout, x, weight, dx, dweight=None, base=None, eps=1e-6, ws=N
         bt, bp, ldb, _ = A.rows("base", base, dev, T, cols, types)
     if ot != rt or bt != rt:
         raise ValueError(f"dx and base have x's type {x.dtype}")
-    wt, (wp,) = _params(dev, cols, dtype, weight=weight)
+    wt, wp = _weight("weight", weight, dev, cols, types)
     dwp = None if dweight is None else A.whole("dweight", dweight, dev, _F32, (cols,))
     sp, sn = _workspace(ws, T, cols, x, dweight is not None, stream)
     A.launch(B.lib().moe_norm_backward, dev, stream, dt, rt, bp, ldb, None, 0, 1.0, wt, None, dt, None, 0, 0, gp, ldg,
@@ -172,7 +185,7 @@ def after_backward(dout, y, dy, dresidual=None, weight=None, dweight=None, gate=
         raise ValueError(f"y: shape {tuple(y.shape)}, expected rows")
     dev, (T, cols), dtype = y.get_device(), y.shape, _block_type("y", y)
     dt, yp, ldy, _ = A.rows("y", y, dev, T, cols)
-    types, rt = {dtype: dt, _F32: B.MOE_T_F32}, None
+    types, rt = _WITH[dtype], None
 
     def residual(name, t):
         nonlocal rt
@@ -198,13 +211,13 @@ def after_backward(dout, y, dy, dresidual=None, weight=None, dweight=None, gate=
     dyt, dyp, lddy, _ = A.rows("dy", dy, dev, T, cols)
     if dyt != dt:
         raise ValueError(f"dy: type {dy.dtype}, y has {y.dtype}")
-    wt, (wp, w2p) = _params(dev, cols, dtype, weight=weight, next_weight=next_weight)
-    gt, gp, gr, gc = _gate("gate", gate, dev, T, cols, dtype)
+    wt, wp, w2p = _weights(weight, next_weight, dev, cols, types)
+    gt, gp, gr, gc = _gate("gate", gate, dev, T, cols, types)
     dgt, dgp, dgr, dgc = dt, None, 0, 0
     if dgate is not None:
         if gate is None or dgate.shape != gate.shape:
             raise ValueError(f"dgate: shape {tuple(dgate.shape)}, expected the gate's")
-        dgt, dgp, dgr, dgc = _gate("dgate", dgate, dev, T, cols, dtype)
+        dgt, dgp, dgr, dgc = _gate("dgate", dgate, dev, T, cols, types)
     dwp = None if dweight is None else A.whole("dweight", dweight, dev, _F32, (cols,))
     dw2 = None if dnext_weight is None else A.whole("dnext_weight", dnext_weight, dev, _F32, (cols,))
     sums = dweight is not None or dnext_weight is not None or (dgate is not None and dgr == 0)

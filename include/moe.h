@@ -664,7 +664,7 @@ int moe_norm(int dtype, const void* y, int64_t ldy, int rtype, const void* resid
  * dweight and dnext_weight fp32 [cols], written whole, may be NULL; dgate
  * (dtype or fp32, may be NULL) has the gate's shape and is summed over what the
  * gate was spread over.  ws: the workspace bytes below, on 4 bytes, where a sum
- * over the rows is asked for. */
+ * over the rows is asked for.  cols <= 8192. */
 size_t moe_norm_backward_workspace_bytes(int64_t T, int64_t cols);
 int moe_norm_backward(int dtype, int rtype, const void* dh, int64_t lddh, const void* y, int64_t ldy, float alpha,
                       int wtype, const void* weight, int gtype, const void* gate, int64_t gate_row, int64_t gate_col,

@@ -140,7 +140,7 @@ def test_norm_refusals(B):
     assert norm(B, T=0) == 0
     need = B.moe_norm_backward_workspace_bytes(4, 64)
     assert 0 < need <= 1 << 20
-    for bad in ((-1, 64), (4, 0), (4, 16385), (2 ** 31, 64), (4 + CUT, 64 + CUT)):
+    for bad in ((-1, 64), (4, 0), (4, 8193), (2 ** 31, 64), (4 + CUT, 64 + CUT)):
         assert B.moe_norm_backward_workspace_bytes(*bad) == 0, bad
     refused(B, norm_backward, [dict(dt=5), dict(rt=1), dict(wt=1), dict(gt=1), dict(dgt=1), dict(T=-1), dict(cols=0),
                                dict(lddh=63), dict(ldy=63), dict(lddn=63), dict(ldh=63), dict(lddy=63), dict(lddr=63),
@@ -148,8 +148,8 @@ def test_norm_refusals(B):
                                dict(dh=None, dn=None), dict(dy=None), dict(h=None), dict(w2=None), dict(w=None),
                                dict(dn=None), dict(eps=-1.0), dict(eps2=float("nan")), dict(ws=None), dict(wsb=need - 1),
                                dict(ws=A[12] + 2)])
-    refused(B, norm_backward, [dict(cols=16385, lddh=20000, ldy=20000, lddn=20000, ldh=20000, lddy=20000, lddr=20000)],
-            B.MOE_E_UNSUPPORTED)
+    refused(B, norm_backward, [dict(cols=n, lddh=20000, ldy=20000, lddn=20000, ldh=20000, lddy=20000, lddr=20000)
+                               for n in (8193, 16384, 16385)], B.MOE_E_UNSUPPORTED)
 
 
 def test_sizes_are_not_cut_to_32_bits(B):

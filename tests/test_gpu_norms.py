@@ -24,6 +24,7 @@ EPS, EPS2 = 1e-5, 1e-3
 PAIRS = [(BF, BF), (BF, F32), (HF, HF), (HF, F32), (F32, F32)]
 WIDTHS = [(1, 1), (1, 2048), (3, 7), (5, 64), (6, 511), (9, 513), (4, 1000), (5, 1025), (7, 2048), (3, 2500), (2, 4096),
           (3, 4100), (2, 8192), (3, 8200), (2, 16384), (70, 300), (0, 32)]
+BACK = [w for w in WIDTHS if w[1] <= 8192]
 GATES = ["none", "token", "channel", "full"]
 
 
@@ -147,7 +148,7 @@ def through(v, d, eps):
 
 @pytest.mark.parametrize("dt,rt", PAIRS)
 @pytest.mark.parametrize("gate", GATES)
-@pytest.mark.parametrize("T,n", WIDTHS + [(1500, 40), (1100, 1500), (600, 4100)])
+@pytest.mark.parametrize("T,n", BACK + [(1500, 40), (1100, 1500), (600, 4100)])
 def test_after_backward(T, n, gate, dt, rt):
     print(f"after backward T={T} n={n} {gate} {dt} {rt}", flush=True)
     rng = np.random.default_rng(T * n + 1)
@@ -202,7 +203,7 @@ def test_after_backward(T, n, gate, dt, rt):
 
 
 @pytest.mark.parametrize("dt,rt", PAIRS)
-@pytest.mark.parametrize("T,n", WIDTHS)
+@pytest.mark.parametrize("T,n", BACK)
 def test_before_backward(T, n, dt, rt):
     print(f"before backward T={T} n={n} {dt} {rt}", flush=True)
     rng = np.random.default_rng(T * n + 2)
