@@ -125,7 +125,8 @@ DEV void load_row(const typename Elem<DT>::type* row, long c, long cols, float (
   for (int i = 0; i < 8; ++i) f[i] = c < cols ? f[i] : 0.0f;
 }
 
-// The same, as they are stored.
+// The same as they are stored, without what waits for them: past cols (EVEN)
+// they are other values of the row, which values() makes zeros.
 template <int DT>
 using Raw = Pack<typename Elem<DT>::type, 8>;
 
@@ -134,7 +135,6 @@ DEV Raw<DT> load_raw(const typename Elem<DT>::type* row, long c, long cols) {
   Raw<DT> r = {};
   if (EVEN) {
     __builtin_memcpy(&r, row + min(c, cols - 8), sizeof(r));
-    if (c >= cols) r = Raw<DT>{};
   } else if (c + 8 <= cols) {
     __builtin_memcpy(&r, row + c, sizeof(r));
   } else {
@@ -146,9 +146,9 @@ DEV Raw<DT> load_raw(const typename Elem<DT>::type* row, long c, long cols) {
 }
 
 template <int DT>
-DEV void values(const Raw<DT>& r, float (&f)[8]) {
+DEV void values(const Raw<DT>& r, bool inside, float (&f)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = Elem<DT>::load(r.v[i]);
+  for (int i = 0; i < 8; ++i) f[i] = inside ? Elem<DT>::load(r.v[i]) : 0.0f;
 }
 
 template <int DT, bool EVEN>
@@ -268,6 +268,17 @@ norm_kernel(NormArgs a) {
   }
 }
 
+__device__ const uint4 NOTHING[2] = {};
+
+template <typename T>
+struct Rows {
+  const T* p;
+  int64_t ld;
+  long cols;
+  DEV Rows(const void* p, int64_t ld, long cols)
+      : p(p ? (const T*)p : (const T*)NOTHING), ld(p ? ld : 0), cols(p ? cols : 8) {}
+};
+
 // With D = dn w', G = gate w and m = mean(D n): <d, G y> = <dh, G y> + (<D, G y>
 // - m <h, G y> / rms(h)) / rms(h), so that one joint sum over the row, of values
 // as they were read, gives both roots and both means.  HELD units of a thread
@@ -316,25 +327,22 @@ norm_bwd_kernel(NormBwdArgs a) {
   struct Unit {
     Raw<RT> d, n;                                       // dh, h
     Raw<DT> g, x;                                       // dn, y
-    float k[8];                                         // gate
   };
-  const bool row_gate = a.gate && (a.gr || !AHEAD);     // its gate comes with a row
+  // What is not there is 8 zeros of every row: loads under a condition would be
+  // waited for where its two sides meet.
+  const Rows<TR> dh(a.dh, a.lddh, cols), h(a.dn ? a.h : nullptr, a.ldh, cols);
+  const Rows<TD> dn(a.dn, a.lddn, cols), y(a.y, a.ldy, cols);
   const auto read = [&](int64_t t, int i, Unit& u) __attribute__((always_inline)) {
-    const long c = column(i);
-    u.d = u.n = Raw<RT>{};
-    u.g = u.x = Raw<DT>{};
-    if (a.dh) u.d = load_raw<RT, EVEN>((const TR*)a.dh + t * a.lddh, c, cols);
-    if (a.dn) {
-      u.n = load_raw<RT, EVEN>((const TR*)a.h + t * a.ldh, c, cols);
-      u.g = load_raw<DT, EVEN>((const TD*)a.dn + t * a.lddn, c, cols);
-    }
-    if (a.y) u.x = load_raw<DT, EVEN>((const TD*)a.y + t * a.ldy, c, cols);
-    if (row_gate) load_gate<DT, EVEN>(a.gate, a.gate_f32, t, a.gr, a.gc, c, cols, u.k);
+    u.d = load_raw<RT, EVEN>(dh.p + t * dh.ld, column(i), dh.cols);
+    u.n = load_raw<RT, EVEN>(h.p + t * h.ld, column(i), h.cols);
+    u.g = load_raw<DT, EVEN>(dn.p + t * dn.ld, column(i), dn.cols);
+    u.x = load_raw<DT, EVEN>(y.p + t * y.ld, column(i), y.cols);
   };
   // AHEAD: the next row is on its way while one is worked on (a CU holds one
   // workgroup of 512), and what is the same for every row stays in registers,
   // as its loads would wait for that row.  4099 rows of 4096 bf16 with a gate
-  // per column: 58 us (201 MB, 3.5 TB/s); 96 without, 82 without the second.
+  // per column: 64 us with the join (202 MB, 3.1 TB/s); 118 without reading ahead
+  // and with a sum after the other, 70 with the loads under conditions.
   float hw[NV][8], hf[NV][8], hk[NV][8];                // w, w', gate
   const auto weights = [&](int i, float (&w)[8], float (&f)[8]) __attribute__((always_inline)) {
 #pragma unroll
@@ -342,24 +350,25 @@ norm_bwd_kernel(NormBwdArgs a) {
     if (a.dn) load_param<DT, EVEN>(a.w2, a.w_f32, column(i), cols, f);
     if (a.w) load_param<DT, EVEN>(a.w, a.w_f32, column(i), cols, w);
   };
-  Unit next[NV], cur[NV];
+  const auto gate = [&](int64_t t, int i, float (&k)[8]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) k[j] = 1.0f;
+    if (a.gate) load_gate<DT, EVEN>(a.gate, a.gate_f32, t, a.gr, a.gc, column(i), cols, k);
+  };
+  Unit next[NV] = {}, cur[NV] = {};
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) hk[i][j] = next[i].k[j] = cur[i].k[j] = 1.0f;
     if (!AHEAD) continue;
     weights(i, hw[i], hf[i]);
-    if (a.gate && !row_gate) load_gate<DT, EVEN>(a.gate, a.gate_f32, 0, a.gr, a.gc, column(i), cols, hk[i]);
+    gate(0, i, hk[i]);
     if (part < a.T) read(part, i, next[i]);
   }
   for (int64_t t = part; t < a.T; t += a.parts) {
     if (AHEAD) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
+        if (a.gr) gate(t, i, hk[i]);
         cur[i] = next[i];
-        if (!row_gate)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) cur[i].k[j] = hk[i][j];
         if (t + a.parts < a.T) read(t + a.parts, i, next[i]);
       }
     } else if (!WIDE) {
@@ -372,19 +381,20 @@ norm_bwd_kernel(NormBwdArgs a) {
     const auto get = [&](int i, Values& v) __attribute__((always_inline)) {
       if (WIDE) read(t, i, cur[0]);
       const Unit& u = cur[WIDE ? 0 : i];
-      values<RT>(u.d, v.d);
-      values<RT>(u.n, v.n);
-      values<DT>(u.g, v.g);
-      values<DT>(u.x, v.x);
+      values<RT>(u.d, column(i) < cols, v.d);
+      values<RT>(u.n, column(i) < cols, v.n);
+      values<DT>(u.g, column(i) < cols, v.g);
+      values<DT>(u.x, column(i) < cols, v.x);
       if (!AHEAD) weights(i, v.w, v.f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (AHEAD) {
           v.w[j] = hw[WIDE ? 0 : i][j];
           v.f[j] = hf[WIDE ? 0 : i][j];
+          v.k[j] = hk[WIDE ? 0 : i][j];
         }
-        v.k[j] = a.gate && column(i) + j < cols ? u.k[j] : 1.0f;
       }
+      if (!AHEAD) gate(t, i, v.k);
     };
     // h^2, D h, y^2, dh G y, D G y, h G y
     float s[6] = {};
