@@ -76,31 +76,33 @@ DEV typename Frag<XT>::type widen(int lo, int hi) {
   return __builtin_bit_cast(typename F::type, v);
 }
 
-// One wave per expert and four tokens; clears the counters of the second
-// kernel, so that the workspace holds nothing from call to call.
+// A workgroup per expert and four tokens, its waves sharing out the columns;
+// clears the counters of the second kernel, so that the workspace holds
+// nothing from call to call.
 template <int XT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(64 * WAVES)
 router_kernel(LayerArgs a, int n_ctl) {
-  const int lane = threadIdx.x & 63;
+  constexpr int STEP = 256 * WAVES;      // columns of a pass of the workgroup
+  __shared__ float lds[WAVES][4];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   if (blockIdx.y == 0)
-    for (int i = blockIdx.x * 256 + threadIdx.x; i < n_ctl; i += gridDim.x * 256) a.ctl[i] = 0;
-  const int e = blockIdx.x * 4 + (threadIdx.x >> 6), t0 = blockIdx.y * 4;
-  if (e >= a.E) return;
+    for (int i = blockIdx.x * 64 * WAVES + tid; i < n_ctl; i += gridDim.x * 64 * WAVES) a.ctl[i] = 0;
+  const int e = blockIdx.x, t0 = blockIdx.y * 4;
   const float* r = a.router + (int64_t)e * a.H;
   float acc[4] = {};
-  for (int c0 = 0; c0 < a.H; c0 += 2048) {
-    float4 rv[8];
-    uint2 xv[8][4];
+  for (int c0 = 0; c0 < a.H; c0 += 4 * STEP) {
+    float4 rv[4];
+    uint2 xv[4][4];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const int h = min(c0 + c * 256 + lane * 4, a.H - 4);
+    for (int c = 0; c < 4; ++c) {
+      const int h = min(c0 + c * STEP + tid * 4, a.H - 4);
       rv[c] = *(const float4*)(r + h);
 #pragma unroll
       for (int i = 0; i < 4; ++i) xv[c][i] = *(const uint2*)(a.x + min(t0 + i, a.T - 1) * a.ldx + h);
     }
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      if (c0 + c * 256 + lane * 4 >= a.H) continue;
+    for (int c = 0; c < 4; ++c) {
+      if (c0 + c * STEP + tid * 4 >= a.H) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         acc[i] += Elem<XT>::load((uint16_t)(xv[c][i].x & 0xffffu)) * rv[c].x;
@@ -110,11 +112,17 @@ router_kernel(LayerArgs a, int n_ctl) {
       }
     }
   }
-  const float b = a.bias ? a.bias[e] : 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float v = wave_sum(acc[i]);
-    if (lane == 0 && t0 + i < a.T) a.z[(t0 + i) * a.E + e] = v + b;
+    if (lane == 0) lds[wave][i] = v;
+  }
+  __syncthreads();
+  if (tid < 4 && t0 + tid < a.T) {
+    float v = 0.0f;
+#pragma unroll
+    for (int q = 0; q < WAVES; ++q) v += lds[q][tid];
+    a.z[(t0 + tid) * a.E + e] = v + (a.bias ? a.bias[e] : 0.0f);
   }
 }
 
@@ -567,15 +575,15 @@ int moe_fp8_layer(int xtype, const void* x, int64_t ldx, const float* router, co
   const LayerArgs a{(const uint16_t*)x, ldx, router, bias, (int)T, (int)E, (int)k, (int)H, (int)I, gate_up,
                     gate_up_scales, down, down_scales, base, ldb, out, ldo, otype, ids, w, (float*)(p + l.z),
                     (unsigned*)(p + l.ctl), (uint16_t*)(p + l.a), (float*)(p + l.part), down_split(k, H, I)};
-  const dim3 rg((unsigned)((E + 3) / 4), (unsigned)((T + 3) / 4));
+  const dim3 rg((unsigned)E, (unsigned)((T + 3) / 4));
   const int64_t tiles = std::max(std::min(E, T * k) * (I / ROWS), H / DOWN_ROWS * a.split);
   const unsigned grid = (unsigned)std::min<int64_t>(tiles, GRID);
   const hipStream_t s = (hipStream_t)stream;
   if (xtype == MOE_T_BF16) {
-    router_kernel<MOE_T_BF16><<<rg, 256, 0, s>>>(a, l.n_ctl);
+    router_kernel<MOE_T_BF16><<<rg, 64 * WAVES, 0, s>>>(a, l.n_ctl);
     layer_kernel<MOE_T_BF16><<<grid, 64 * WAVES, 0, s>>>(a);
   } else {
-    router_kernel<MOE_T_F16><<<rg, 256, 0, s>>>(a, l.n_ctl);
+    router_kernel<MOE_T_F16><<<rg, 64 * WAVES, 0, s>>>(a, l.n_ctl);
     layer_kernel<MOE_T_F16><<<grid, 64 * WAVES, 0, s>>>(a);
   }
   return launched();

@@ -1,9 +1,9 @@
 """GPU parity of the norms around a block, forward and backward, with the
 float64 oracle.
 
-Forward: a mean of n squares is off by at most (n / 8 + 16) u of itself (u =
-2^-24 a rounding; a thread sums up to 16 squares, waves and their sums less than
-16 more: 40 roundings cover every width), its root and quotient by 3 more, so a
+Forward: a mean of n squares is off by at most 40 u of itself (u = 2^-24 a
+rounding; a thread sums up to 16 squares, waves and their sums add less than 16
+more roundings, so 40 cover every width), its root and quotient by 3 more, so a
 normed value by N = 32 u of itself; h by 3 roundings of its terms' magnitudes,
 and half a step of its type.  The next norm is checked on the h that was
 stored.  Backward: the mean of products is off by 44 u of the mean of their
