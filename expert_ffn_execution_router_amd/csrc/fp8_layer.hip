@@ -429,10 +429,11 @@ DEV void down_tile(const LayerArgs& a, Routed& s, int tile, int p, F wait) {
   }
 }
 
-// Workgroups take gate/up tiles blockIdx, + gridDim, .. and then down tiles the
-// same way.  A down tile waits until every gate/up tile is finished, however
+// Workgroups take gate/up tiles blockIdx, + gridDim, .. and then down tiles from
+// the last workgroup backwards, so that with few tokens those without a gate/up
+// tile have the down weights on their way while the others work.  A down tile waits until every gate/up tile is finished, however
 // few workgroups are resident: each gate/up tile is claimed before it is begun,
-// and a workgroup takes what is left unclaimed of the others' before it waits.
+// and one with a down tile takes what is left unclaimed before it waits.
 // So what it waits for is held by running workgroups, which wait for nothing
 // until they have finished it.  The last one to finish raises the flags: each
 // is polled by few workgroups, and the counter by none.
@@ -473,6 +474,8 @@ layer_kernel(LayerArgs a) {
     if (mine == 0) gate_up(tile);
     __syncthreads();
   }
+  const int d0 = gridDim.x - 1 - blockIdx.x;
+  if (d0 >= tiles_b * a.split) return;
   for (;;) {
     if (tid == 0) s.pick = 0xffffffffu;
     __syncthreads();
@@ -495,7 +498,7 @@ layer_kernel(LayerArgs a) {
     __syncthreads();
   }
   bool ready = false;
-  for (int d = blockIdx.x; d < tiles_b * a.split; d += gridDim.x) {
+  for (int d = d0; d < tiles_b * a.split; d += gridDim.x) {
     down_tile(a, s, d % tiles_b, d / tiles_b, [&] {
       if (ready) return;
       if (tid == 0) {
@@ -512,10 +515,13 @@ layer_kernel(LayerArgs a) {
 
 int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
-int down_split(int64_t k, int64_t H, int64_t I) {
-  // about 512 down tiles, each with an entry for every wave at least
-  const int64_t tiles = H / DOWN_ROWS, entries = k * (I / 128);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / tiles, entries / WAVES, 8}));
+// Down tiles for each 32 rows: about 512 in all or, where that leaves at least
+// half as many, one for each workgroup without a gate/up tile (one token of 8
+// experts, 2048 x 768: SPLIT), with an entry for every wave at least.
+int down_split(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {
+  const int64_t tiles = H / DOWN_ROWS, entries = k * (I / 128), many = 512 / tiles;
+  const int64_t free = (GRID - std::min(E, T * k) * (I / ROWS)) / tiles;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({2 * free >= many ? std::min(free, many) : many, entries / WAVES, 8}));
 }
 
 bool sizes_ok(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {
@@ -534,7 +540,7 @@ Layout layout(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {
   l.ctl = up256(T * E * 4);
   l.a = l.ctl + up256(l.n_ctl * 4);
   l.part = l.a + up256(3 * T * k * I * 2);
-  l.end = l.part + down_split(k, H, I) * H * MAX_T * 4;
+  l.end = l.part + down_split(T, E, k, H, I) * H * MAX_T * 4;
   return l;
 }
 
@@ -574,9 +580,9 @@ int moe_fp8_layer(int xtype, const void* x, int64_t ldx, const float* router, co
   uint8_t* p = (uint8_t*)ws;
   const LayerArgs a{(const uint16_t*)x, ldx, router, bias, (int)T, (int)E, (int)k, (int)H, (int)I, gate_up,
                     gate_up_scales, down, down_scales, base, ldb, out, ldo, otype, ids, w, (float*)(p + l.z),
-                    (unsigned*)(p + l.ctl), (uint16_t*)(p + l.a), (float*)(p + l.part), down_split(k, H, I)};
+                    (unsigned*)(p + l.ctl), (uint16_t*)(p + l.a), (float*)(p + l.part), down_split(T, E, k, H, I)};
   const dim3 rg((unsigned)E, (unsigned)((T + 3) / 4));
-  const int64_t tiles = std::max(std::min(E, T * k) * (I / ROWS), H / DOWN_ROWS * a.split);
+  const int64_t tiles = std::min(E, T * k) * (I / ROWS) + H / DOWN_ROWS * a.split;
   const unsigned grid = (unsigned)std::min<int64_t>(tiles, GRID);
   const hipStream_t s = (hipStream_t)stream;
   if (xtype == MOE_T_BF16) {
