@@ -9,14 +9,22 @@
 
 typedef float f32x8_t __attribute__((ext_vector_type(8)));
 
-// Order of |v| as integers: NaN above infinity above every finite value.
-DEV uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// The larger; NaN if either is (of equal values, zeros of either sign).
+DEV float maximum(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
+template <int N>
+DEV float abs_max(const float (&v)[N]) {
+  float m = fabsf(v[0]);
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = maximum(m, fabsf(v[i]));
+  return m;
+}
 
 struct GroupScale {
   float inv, scale;
 };
-DEV GroupScale group_scale(uint32_t amax) {
-  const float a = __uint_as_float(max(amax, (127u - 100u) << 23));
+DEV GroupScale group_scale(float amax) {
+  const float a = maximum(amax, 0x1p-100f);
   return GroupScale{448.0f / a, a / 448.0f};
 }
 
@@ -26,12 +34,33 @@ DEV uint32_t codes4(float a, float b, float c, float d, float inv) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, w, true);
 }
 
+template <int CTRL>
+DEV float dpp(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+
 // Largest value over the lane's row of 16 lanes, in all of them.
-DEV uint32_t row16_max(uint32_t v) {
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, false));   // rotated by 8
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, false));
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xf, 0xf, false));
-  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xf, 0xf, false));
+DEV float row16_max(float v) {
+  v = maximum(v, dpp<0x128>(v));         // rotated by 8
+  v = maximum(v, dpp<0x124>(v));
+  v = maximum(v, dpp<0x122>(v));
+  return maximum(v, dpp<0x121>(v));
+}
+
+// The same over lanes l, l ^ 16, l ^ 32, l ^ 48.
+DEV float lanes_max(float v) {
+  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+  uint32_t b = __float_as_uint(v);
+  u32x2_t p = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane16_swap(b, b, false, false));
+  b = __float_as_uint(maximum(__uint_as_float(p[0]), __uint_as_float(p[1])));
+  p = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_permlane32_swap(b, b, false, false));
+  return maximum(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+
+// Lane I of the lane's quad.
+template <int I>
+DEV float quad_lane(float v) {
+  return dpp<I * 0x55>(v);
 }
 
 // Up to 8 values from column c on; zeros from column cols on.

@@ -10,6 +10,8 @@ struct QuantArgs {
   int64_t ldx, x_rows, x_step;     // x_step: values from one matrix to the next (weights)
   const int32_t* row_map;
   int map_div;
+  uint32_t div_mul;                // n / map_div = n div_mul >> div_shift, for n < 2^31 (n without map_div)
+  int div_shift;
   int64_t R, K;
   uint8_t* codes;                  // [R][Kp]
   float* scales;                   // rows: [Kp/128][R]; weights: [Rp/128][Kp/128]
@@ -30,58 +32,70 @@ constexpr int Q_THREADS = 512, Q_SPAN = 4;       // rows of a thread
 
 DEV int tile_word(int c, int q) { return c * 32 + (((q >> 2) ^ (c >> 3)) & 7) * 4 + (q & 3); }
 
+__device__ const uint4 NOTHING[2] = {};          // eight zeros of any type
+
 template <int DT, int MODE, bool GATED>
 __global__ void __launch_bounds__(Q_THREADS)
 quant_kernel(QuantArgs a) {
   typedef typename Elem<DT>::type T;
   constexpr int WAVES = Q_THREADS / 64, S = Q_SPAN;
-  __shared__ uint32_t part[WAVES][128];
+  __shared__ float part[WAVES][128];
   __shared__ __align__(16) uint32_t tile[(MODE & Q_ROWS) && !(MODE & Q_COLS) ? 4 : 128 * 32];
   const int tid = threadIdx.x, q = tid >> 4, l = tid & 15, wave = tid >> 6;
   const unsigned ct = blockIdx.x % (unsigned)a.col_tiles, rest = blockIdx.x / (unsigned)a.col_tiles;
   const unsigned rt = rest % (unsigned)a.row_tiles, e = rest / (unsigned)a.row_tiles;
-  const int64_t r0 = (int64_t)rt * 128 + S * q, c0 = (int64_t)ct * 128 + 8 * l;
+  const int r0 = (int)rt * 128 + S * q, c0 = (int)ct * 128 + 8 * l, R = (int)a.R;
   const int64_t Kp = (int64_t)a.col_tiles * 128, Rp = (int64_t)a.row_tiles * 128;
   const T* x = (const T*)a.x + e * a.x_step;
-  float v[S][8];
+  float v[S][8], u[S][8];
   unsigned keep = 0;               // bit i: row i is written
-  int64_t src[S];                  // its row of x, -1: zeros
+  int src[S];                      // its row of x, -1: zeros
   int m[S];
 #pragma unroll
-  for (int i = 0; i < S; ++i) m[i] = (int)(r0 + i);
-  if (a.row_map) {                 // loads without a branch between them
+  for (int i = 0; i < S; ++i) m[i] = r0 + i;
+  if (a.row_map)
 #pragma unroll
-    for (int i = 0; i < S; ++i) m[i] = a.row_map[min(r0 + i, a.R - 1)];
-  }
-#pragma unroll
-  for (int i = 0; i < S; ++i) {
-    src[i] = -1;
-    if (r0 + i >= a.R) continue;
-    if (!a.row_map || m[i] >= -1) keep |= 1u << i;
-    if (m[i] < 0) continue;
-    int64_t at = m[i];
-    if (a.row_map) at = a.map_div ? (int64_t)((unsigned)m[i] / (unsigned)a.map_div) : r0 + i;
-    if (at < a.x_rows) src[i] = at;
-  }
+    for (int i = 0; i < S; ++i) m[i] = a.row_map[min(r0 + i, R - 1)];
 #pragma unroll
   for (int i = 0; i < S; ++i) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-    if (src[i] >= 0) load8<DT>(x + src[i] * a.ldx, c0, a.K, v[i]);
+    const uint32_t n = a.map_div ? (uint32_t)m[i] : (uint32_t)(r0 + i);
+    const int at = (int)((uint64_t)n * a.div_mul >> a.div_shift);
+    if (r0 + i < R && m[i] >= -1) keep |= 1u << i;
+    src[i] = r0 + i < R && m[i] >= 0 && at < (int)a.x_rows ? at : -1;
   }
-  if (GATED) {
-    float u[S][8];
+  if ((int64_t)ct * 128 + 128 <= a.K) {
+    Pack<T, 8> raw[S], raw_u[S];   // loads without a branch between them
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) u[i][j] = 0.0f;
-      if (src[i] >= 0) load8<DT>(x + src[i] * a.ldx + a.K, c0, a.K, u[i]);
+      const T* from = x + (uint64_t)(uint32_t)src[i] * (uint64_t)a.ldx + c0;
+      const T* up = from + a.K;
+      from = src[i] >= 0 ? from : (const T*)NOTHING;
+      up = src[i] >= 0 ? up : (const T*)NOTHING;
+      __builtin_memcpy(&raw[i], from, sizeof(raw[i]));
+      if (GATED) __builtin_memcpy(&raw_u[i], up, sizeof(raw_u[i]));
     }
 #pragma unroll
     for (int i = 0; i < S; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = silu(v[i][j]) * u[i][j];
+      for (int j = 0; j < 8; ++j) {
+        v[i][j] = Elem<DT>::load(raw[i].v[j]);
+        if (GATED) u[i][j] = Elem<DT>::load(raw_u[i].v[j]);
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = u[i][j] = 0.0f;
+      if (src[i] < 0) continue;
+      load8<DT>(x + (int64_t)src[i] * a.ldx, c0, a.K, v[i]);
+      if (GATED) load8<DT>(x + (int64_t)src[i] * a.ldx + a.K, c0, a.K, u[i]);
+    }
   }
+  if (GATED)
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = silu(v[i][j]) * u[i][j];
   // the words of the transposed codes to their rows
   const auto store_t = [&](uint8_t* to) {
     __syncthreads();
@@ -94,57 +108,65 @@ quant_kernel(QuantArgs a) {
     }
   };
   if (MODE & Q_ROWS) {
+    // lane 4 n + i of a group takes over row i of its quad, joins it with the
+    // other quads' and gives the scales back: two divisions in place of eight
+    static_assert(S == 4, "a row for each lane of a quad");
+    float mx[S];
+#pragma unroll
+    for (int i = 0; i < S; ++i) mx[i] = abs_max(v[i]);
+    const bool odd = l & 1, high = l & 2;
+    const float lo = maximum(odd ? mx[1] : mx[0], dpp<0xB1>(odd ? mx[0] : mx[1]));
+    const float hi = maximum(odd ? mx[3] : mx[2], dpp<0xB1>(odd ? mx[2] : mx[3]));
+    float m4 = maximum(high ? hi : lo, dpp<0x4E>(high ? lo : hi));
+    m4 = maximum(m4, dpp<0x124>(m4));
+    m4 = maximum(m4, dpp<0x128>(m4));
+    const GroupScale s = group_scale(m4);
+    const float inv[S] = {quad_lane<0>(s.inv), quad_lane<1>(s.inv), quad_lane<2>(s.inv), quad_lane<3>(s.inv)};
+    uint8_t* to = a.codes + (int64_t)r0 * Kp + c0;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      uint32_t mx = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) mx = max(mx, abs_bits(v[i][j]));
-      const GroupScale s = group_scale(row16_max(mx));
       if (!((keep >> i) & 1)) continue;
-      const uint2 w = {codes4(v[i][0], v[i][1], v[i][2], v[i][3], s.inv),
-                       codes4(v[i][4], v[i][5], v[i][6], v[i][7], s.inv)};
-      *(uint2*)(a.codes + (r0 + i) * Kp + c0) = w;
-      if (l == 0) a.scales[(int64_t)ct * a.R + r0 + i] = s.scale;
+      const uint2 w = {codes4(v[i][0], v[i][1], v[i][2], v[i][3], inv[i]),
+                       codes4(v[i][4], v[i][5], v[i][6], v[i][7], inv[i])};
+      *(uint2*)(to + i * Kp) = w;
     }
+    if (l < S && ((keep >> l) & 1)) a.scales[(int64_t)ct * a.R + r0 + l] = s.scale;
   }
   if (MODE & Q_COLS) {
     if (a.row_map && !__syncthreads_or(keep != 0)) return;      // nothing but rows behind the last segment
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      uint32_t mx = 0;
-#pragma unroll
-      for (int i = 0; i < S; ++i) mx = max(mx, abs_bits(v[i][j]));
-      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16, 64));
-      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32, 64));
+      const float mx = lanes_max(abs_max({v[0][j], v[1][j], v[2][j], v[3][j]}));
       if ((tid & 63) < 16) part[wave][8 * l + j] = mx;
+    }
+    __syncthreads();
+    if (tid < 128) {
+      float mx = part[0][tid];
+#pragma unroll
+      for (int w = 1; w < WAVES; ++w) mx = maximum(mx, part[w][tid]);
+      const GroupScale s = group_scale(mx);
+      const int64_t col = (int64_t)ct * 128 + tid;
+      if (col < a.K) a.scales_t[(int64_t)rt * a.K + col] = s.scale;
+      part[0][tid] = s.inv;
     }
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int c = 8 * l + j;
-      uint32_t mx = 0;
-#pragma unroll
-      for (int w = 0; w < WAVES; ++w) mx = max(mx, part[w][c]);
-      const GroupScale s = group_scale(mx);
-      tile[tile_word(c, q)] = codes4(v[0][j], v[1][j], v[2][j], v[3][j], s.inv);
-      if (q == 0 && c0 + j < a.K) a.scales_t[(int64_t)rt * a.K + c0 + j] = s.scale;
+      tile[tile_word(c, q)] = codes4(v[0][j], v[1][j], v[2][j], v[3][j], part[0][c]);
     }
     store_t(a.codes_t);
   }
   if (MODE & Q_BLOCKS) {
-    uint32_t mx = 0;
+    float mx = abs_max(v[0]);
 #pragma unroll
-    for (int i = 0; i < S; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) mx = max(mx, abs_bits(v[i][j]));
-    mx = row16_max(mx);
-    mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16, 64));
-    mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32, 64));
+    for (int i = 1; i < S; ++i) mx = maximum(mx, abs_max(v[i]));
+    mx = lanes_max(row16_max(mx));
     if ((tid & 63) == 0) part[wave][0] = mx;
     __syncthreads();
-    mx = 0;
+    mx = part[0][0];
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) mx = max(mx, part[w][0]);
+    for (int w = 1; w < WAVES; ++w) mx = maximum(mx, part[w][0]);
     const GroupScale s = group_scale(mx);
     const int64_t blocks = (int64_t)a.row_tiles * a.col_tiles;
     if (a.codes) {
@@ -226,7 +248,11 @@ int moe_fp8_quantize(int dtype, const void* x, int64_t ldx, int64_t x_rows, cons
   if (x_rows && !x) return bad(MOE_E_INVAL, "null argument");
   if (((uintptr_t)codes | (uintptr_t)codes_t) % 16) return bad(MOE_E_INVAL, "codes start on 16 bytes");
   const int64_t Kp = pad128(cols), Rp = pad128(rows);
-  QuantArgs a{x, ldx, x_rows, 0, row_map, row_map ? (int)map_div : 1, rows, cols, codes, scales, codes_t, scales_t,
+  const int64_t div = row_map && map_div ? map_div : 1;
+  int log2 = 0;                    // ceil(log2(div)); with m = floor(2^(31 + log2) / div) + 1, m div - 2^(31 + log2) <= 2^log2
+  while (((int64_t)1 << log2) < div) ++log2;
+  const uint32_t div_mul = (uint32_t)((((uint64_t)1 << (31 + log2)) / (uint64_t)div) + 1);
+  QuantArgs a{x, ldx, x_rows, 0, row_map, row_map ? (int)map_div : 0, div_mul, 31 + log2, rows, cols, codes, scales, codes_t, scales_t,
               (int)(Rp / 128), (int)(Kp / 128)};
   if ((int64_t)a.row_tiles * a.col_tiles > MAX_TILES) return bad(MOE_E_UNSUPPORTED, "too many values");
   if (outputs_shared({span(codes, rows * Kp), span(scales, Kp / 128 * rows * 4), span(codes_t, cols * Rp),
@@ -256,7 +282,7 @@ int moe_fp8_quantize_weights(int dtype, const void* w, int64_t E, int64_t N, int
                       span(scales_t, E * blocks * 4)},
                      {span(w, E * N * K * b)}))
     return shared();
-  const QuantArgs a{w, K, N, N * K, nullptr, 1, N, K, codes, scales, codes_t, scales_t, (int)(Np / 128),
+  const QuantArgs a{w, K, N, N * K, nullptr, 0, 0x80000001u, 31, N, K, codes, scales, codes_t, scales_t, (int)(Np / 128),
                     (int)(Kp / 128)};
   return launch_quant<Q_BLOCKS, false>(dtype, a, E, (hipStream_t)stream);
 }

@@ -256,10 +256,7 @@ norm_kernel(NormArgs a) {
       if (c < cols) store8<DT>((TD*)a.next + t * a.ldn, c, cols, h[i]);
       continue;
     }
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, abs_bits(h[i][j]));
-    const GroupScale q = group_scale(row16_max(m));
+    const GroupScale q = group_scale(row16_max(abs_max(h[i])));
     if (c / 128 * 128 >= cols) continue;             // whole groups: the last one's tail is zeros
     const uint2 v = {codes4(h[i][0], h[i][1], h[i][2], h[i][3], q.inv),
                      codes4(h[i][4], h[i][5], h[i][6], h[i][7], q.inv)};
