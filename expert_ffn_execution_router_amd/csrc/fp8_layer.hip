@@ -7,6 +7,10 @@
 //
 // The weights are met by 16-bit activations: codes become bf16 or fp16
 // exactly, products are exact, sums fp32.
+// The chosen experts' bytes are the floor.  One token of 8 experts (2048 x 768,
+// 39 MB): 28.7 us, a chain of waits: the router 4.7, the choice 4, gate/up
+// weights 8, their hand-over 3, down 7 with its join.  16 tokens of 6 of 256
+// (4096 x 2048, 2.1 GB): 465 us, 4.5 TB/s.
 #include "e4m3.h"
 #include "op_host.h"
 #include "route_dev.h"
@@ -517,11 +521,13 @@ int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
 // Down tiles for each 32 rows: about 512 in all or, where that leaves at least
 // half as many, one for each workgroup without a gate/up tile (one token of 8
-// experts, 2048 x 768: SPLIT), with an entry for every wave at least.
+// experts, 2048 x 768: 33.3 us with its launches, 34.9 with 512), with an entry
+// for every wave at least.
 int down_split(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {
   const int64_t tiles = H / DOWN_ROWS, entries = k * (I / 128), many = 512 / tiles;
   const int64_t free = (GRID - std::min(E, T * k) * (I / ROWS)) / tiles;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({2 * free >= many ? std::min(free, many) : many, entries / WAVES, 8}));
+  const int64_t parts = 2 * free >= many ? std::min(free, many) : many;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({parts, entries / WAVES, 8}));
 }
 
 bool sizes_ok(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {

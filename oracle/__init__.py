@@ -9,6 +9,8 @@ HIP library (expert_ffn_execution_router_amd) and never imports it.
   cache    global LRU slot model, q* split, link-bound prefill time
   dispatch pairs sorted by expert, rows there and back, and the gradients
   w4       products with 4-bit weights and group scales
+  fp8      E4M3 codes with scales per 128, their products and gradients
+  norms    the norms around a block with gate and residual scale, and gradients
 
 Every function is pinned by tests/test_oracle_*.py against values that do not
 come from the oracle itself (format definitions, hand-computed worked
