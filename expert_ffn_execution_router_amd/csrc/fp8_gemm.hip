@@ -183,6 +183,8 @@ DEV void dma4(const void* src, lds_u8_t* dst) {
   __builtin_amdgcn_global_load_lds((gbl_void_t*)src, (lds_void_t*)dst, 4, 0, 0);
 }
 
+typedef float f32x4u_t __attribute__((ext_vector_type(4), aligned(4)));
+
 struct Item {
   int e, rows, cols, g0, g1;
   int64_t r0, c0;
@@ -411,6 +413,32 @@ tile_kernel(MmArgs a) {
   // each, -1 where their number is another (a ragged edge, sums).
   const auto store = [&](const Item& t) {
     const int blocks = min(max((t.rows - 16 * SUB * wm + 15) / 16, 0), SUB);
+    if (DEPTH && !a.add && t.cols == C::BN) {
+      // lanes lr and lr ^ 8 exchange halves, so that a store writes whole lines
+      // of 128 bytes of 8 rows; once, and more than the caches hold
+      const bool low = lr < 8;
+      const int r = 16 * SUB * wm + (lr & 7);
+      float* const to = (float*)a.out + (t.e * a.R + t.r0 + r) * a.ldo + t.c0 + 16 * NS * wn + (low ? 0 : 16) + 4 * lg;
+#pragma unroll
+      for (int j = 0; j < SUB; ++j) {
+        if (j >= blocks) break;
+#pragma unroll
+        for (int i = 0; i < NS; i += 2) {
+          f32x4u_t up, down;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float mine = low ? acc[i][j][u] : acc[i + 1][j][u];
+            const float other = dpp<0x128>(low ? acc[i + 1][j][u] : acc[i][j][u]);
+            up[u] = low ? mine : other;
+            down[u] = low ? other : mine;
+          }
+          float* const at = to + 16 * j * a.ldo + 16 * i;
+          if (r + 16 * j < t.rows) __builtin_nontemporal_store(up, (f32x4u_t*)at);
+          if (r + 16 * j + 8 < t.rows) __builtin_nontemporal_store(down, (f32x4u_t*)(at + 8 * a.ldo));
+        }
+      }
+      return min(max((t.rows - 16 * SUB * wm + 7) / 16, 0), SUB);      // a last one of 8 rows has half the stores
+    }
 #pragma unroll
     for (int j = 0; j < SUB; ++j) {
       if (j >= blocks) break;
@@ -426,8 +454,7 @@ tile_kernel(MmArgs a) {
           for (int u = 0; u < 4; ++u)
             if (u < n) v[u] += ((const float*)a.out)[at + c + u];
         if (n >= 4) {
-          if (DEPTH) {                               // written once, larger than the caches
-            typedef float f32x4u_t __attribute__((ext_vector_type(4), aligned(4)));
+          if (DEPTH) {
             __builtin_nontemporal_store(f32x4u_t{v[0], v[1], v[2], v[3]}, (f32x4u_t*)((float*)a.out + at + c));
           } else if (a.otype == MOE_T_F32) {
             __builtin_memcpy((float*)a.out + at + c, &v, 16);
@@ -443,7 +470,7 @@ tile_kernel(MmArgs a) {
         }
       }
     }
-    return t.cols == C::BN && !(DEPTH && a.add) ? blocks : -1;
+    return t.cols == C::BN && !DEPTH ? blocks : -1;
   };
   // Loads and stores are counted in the order of issue.  The unit that is
   // waited for was loaded before `newer` other units and, for NST - 1 units
