@@ -185,6 +185,13 @@ DEV void dma4(const void* src, lds_u8_t* dst) {
 
 typedef float f32x4u_t __attribute__((ext_vector_type(4), aligned(4)));
 
+// p[i] of an input, i the same in the wave, by a scalar load: a vector load's
+// wait would be for every load and store in flight.
+DEV int constant(const int32_t* p, int i) {
+  typedef const __attribute__((address_space(4))) int32_t* constant_t;
+  return ((constant_t)(uintptr_t)p)[__builtin_amdgcn_readfirstlane(i)];
+}
+
 struct Item {
   int e, rows, cols, g0, g1;
   int64_t r0, c0;
@@ -256,8 +263,8 @@ tile_kernel(MmArgs a) {
       q = i - e * dense_m * ntiles;
       const int x = e / a.split, s = e - x * a.split;      // e: of the outputs
       if (a.offsets) {
-        o.g0 = min(max(a.offsets[x], 0) / 128, a.groups);
-        o.g1 = max(min(max(a.offsets[x + 1], 0) / 128, a.groups), o.g0);
+        o.g0 = min(max(constant(a.offsets, x), 0) / 128, a.groups);
+        o.g1 = max(min(max(constant(a.offsets, x + 1), 0) / 128, a.groups), o.g0);
       }
       const int64_t n = o.g1 - o.g0;
       o.g1 = o.g0 + (int)(n * (s + 1) / a.split);
@@ -271,8 +278,9 @@ tile_kernel(MmArgs a) {
       }
       nm = pref[e + 1] - pref[e];
       q = i - pref[e] * ntiles;
-      first = (int)min(max((int64_t)a.offsets[e], (int64_t)0), a.R);
-      const int64_t many = a.counts ? (int64_t)a.counts[e] : (int64_t)a.offsets[e + 1] - a.offsets[e];
+      const int64_t from = constant(a.offsets, e);
+      first = (int)min(max(from, (int64_t)0), a.R);
+      const int64_t many = a.counts ? (int64_t)constant(a.counts, e) : constant(a.offsets, e + 1) - from;
       end = (int)max(min(first + many, a.R), (int64_t)first);
     }
     nm = __builtin_amdgcn_readfirstlane(nm);
