@@ -159,9 +159,10 @@ stream_kernel(MmArgs a, int row_blocks) {
 // a fused multiply-add per result beside its matrix instruction, and the two
 // hardly overlap; deeper stages, wave priorities and fixed schedules changed
 // nothing.  Experts of 4096 tokens on 4.6 GB of weights in 980 us (4.7 TB/s).
-// Gradients of 128 experts, 1536 x 2048, in 862 us (1.6 GB written; the stores
-// alone take about 400, conversions and products 400, partly side by side): the
-// codes are converted to fp16, as fp32 results need every bit.
+// Gradients of 128 experts, 1536 x 2048, in 818 us (1.6 GB written; the stores
+// alone take 280, loads and products 600, loads and stores 535: the memory path
+// of a CU and its vector work are shared by all three): the codes are converted
+// to fp16, as fp32 results need every bit.
 template <bool DEPTH, bool EXACT, int SUB, int NS>
 struct Tile {
   static constexpr int BM = 32 * SUB, BN = 64 * NS;
@@ -186,7 +187,7 @@ DEV void dma4(const void* src, lds_u8_t* dst) {
 typedef float f32x4u_t __attribute__((ext_vector_type(4), aligned(4)));
 
 // p[i] of an input, i the same in the wave, by a scalar load: a vector load's
-// wait would be for every load and store in flight.
+// wait would be for every load and store in flight (gradients 862 -> 818 us).
 DEV int constant(const int32_t* p, int i) {
   typedef const __attribute__((address_space(4))) int32_t* constant_t;
   return ((constant_t)(uintptr_t)p)[__builtin_amdgcn_readfirstlane(i)];
@@ -423,9 +424,9 @@ tile_kernel(MmArgs a) {
     const int blocks = min(max((t.rows - 16 * SUB * wm + 15) / 16, 0), SUB);
     if (DEPTH && !a.add && t.cols == C::BN) {
       // lanes lr and lr ^ 8 exchange halves, so that a store writes whole lines
-      // of 128 bytes of 8 rows (half lines of 16: 900 us in place of 862 for the
-      // gradients above; with 16-bit results it changes nothing); once, and more
-      // than the caches hold
+      // of 128 bytes of 8 rows (half lines of 16 took 4% longer for the gradients
+      // above; with 16-bit results it changes nothing); once, and more than the
+      // caches hold, so past them (3% longer without)
       const bool low = lr < 8;
       const int r = 16 * SUB * wm + (lr & 7);
       float* const to = (float*)a.out + (t.e * a.R + t.r0 + r) * a.ldo + t.c0 + 16 * NS * wn + (low ? 0 : 16) + 4 * lg;
