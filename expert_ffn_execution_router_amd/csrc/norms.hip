@@ -704,7 +704,8 @@ int moe_norm_backward(int dtype, int rtype, const void* dh, int64_t lddh, const 
                       set_g, T, (int)cols, (int)parts, eps, next_eps, wtype == MOE_T_F32, gtype == MOE_T_F32,
                       dgtype == MOE_T_F32};
   const hipStream_t s = (hipStream_t)stream;
-  rc = by_types(dtype, rtype, [&](auto d, auto r) {
+  if (T == 0) j.parts = 0;                             // sums of nothing: no row's memory is touched
+  else rc = by_types(dtype, rtype, [&](auto d, auto r) {
     return by_bwd_width(cols, [&](auto tpr, auto nv) {
       const int64_t blocks = tpr.value == 64 ? (parts + 3) / 4 : parts;
       const unsigned threads = tpr.value == 64 ? 256 : tpr.value;
