@@ -283,7 +283,8 @@ DEV void gate_up_tile(const LayerArgs& a, Routed& s, int slot, int f0) {
   float v[2];
   join_waves<2>(acc, s, v);
   const float h = silu(v[0]) * v[1];
-  const uint16_t hi = Elem<MOE_T_BF16>::store(h);
+  uint16_t hi = Elem<MOE_T_BF16>::store(h);
+  if ((hi & 0x7fff) == 0x7f80 && fabsf(h) < INFINITY) --hi;      // the largest there is: the others hold the rest
   const float r1 = fabsf(h) < INFINITY ? h - bf16_bits_to_f32(hi) : 0.0f;
   const uint16_t mid = Elem<MOE_T_BF16>::store(r1), low = Elem<MOE_T_BF16>::store(r1 - bf16_bits_to_f32(mid));
   // thread (wave i, lane) has feature 4 lg + i: two neighbours make a word

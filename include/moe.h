@@ -632,7 +632,9 @@ int moe_fp8_weight_gradient(const uint8_t* dy_t, const float* dy_scales, const u
  * rows first) and down codes [E][H][I] with block scales as
  * moe_fp8_quantize_weights gives them; base fp32 [T, H] or NULL; out x's type
  * or fp32; ids int32 and w fp32 [T, k] are outputs.  Weights are met by the
- * 16-bit rows, activations between the products keep 24 bits.  E <= 256, k <=
+ * 16-bit rows, activations between the products keep 24 bits.  Sums over 128
+ * are formed before their scale: x and the activations stay below 2^112, where
+ * 128 products with codes of up to 448 pass fp32's range.  E <= 256, k <=
  * 8, H and I multiples of 128 up to 32768.  ws: the workspace bytes below, on
  * 16 bytes; it holds nothing between calls, and two calls that may run at the
  * same time need one each. */
