@@ -1,5 +1,5 @@
-"""Checks and launch plumbing shared by the operator modules (dispatch, w4):
-a wrong type, shape, stride or device is an error here, before any kernel.
+"""Checks and launch plumbing shared by the operator modules: a wrong type,
+shape, stride or device is an error here, before any kernel.
 
 A single-token call's kernels take a few microseconds, so the checks read
 each tensor property once and compare plain integers."""
@@ -60,6 +60,18 @@ def whole(name, t, dev, dtype, shape=None):
     if dtype is not _I32 and t.requires_grad and _grad_enabled():
         _no_graph(name)
     return t.data_ptr()
+
+
+def workspace(ws, need, x, stream):
+    """Address and size of ws, or of one of need bytes on x's device, of the
+    stream that will use it."""
+    if ws is None and need and x.get_device() >= 0:
+        if stream is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+        else:
+            with torch.cuda.stream(stream):
+                ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+    return (None, 0) if ws is None else (whole("ws", ws, x.get_device(), torch.uint8), ws.numel())
 
 
 def overlaps(name):

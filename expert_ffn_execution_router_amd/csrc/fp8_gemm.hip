@@ -55,9 +55,9 @@ DEV void store_value(void* out, int64_t at, int otype, float v) {
 // bytes twice per group: whole 128-byte lines of a row) and join their sums in
 // LDS.  The matrix instruction's columns are rows of P and its rows columns of
 // Q, so a lane ends with four neighbours of one row.  The 8-bit instruction's
-// sum of neighbouring products keeps fewer bits than fp32, and here
-// the weights' bytes are the bound, so the codes are multiplied as fp16, which
-// is exact.  32 rows, 4096 x 4096: 9.8 us alone (17 MB, 1.8 TB/s: a launch, the
+// sum of neighbouring products keeps fewer bits than fp32, and here the
+// weights' bytes are the bound, so the codes are multiplied as fp16, which is
+// exact.  32 rows, 4096 x 4096: 9.8 us alone (17 MB, 1.8 TB/s: a launch, the
 // loads' latency twice and the join), 34 with the weights through LDS.
 constexpr int STREAM_WAVES = 8;
 
@@ -155,19 +155,23 @@ stream_kernel(MmArgs a, int row_blocks) {
 // all banks; the scales behind them.  Every wave issues the same number of
 // loads for a group, so the wait for a stage leaves exactly the later ones
 // outstanding.  Rows past an edge repeat the last one and are not stored.
-// 8192 x 4096 x 4096 in 173 us (1.6 PFLOP/s): each 128 of the summed axis costs
-// a fused multiply-add per result beside its matrix instruction, and the two
-// hardly overlap; deeper stages, wave priorities and fixed schedules changed
-// nothing.  The 8-bit instruction adds 8 neighbouring products at a time and
-// drops of each what is under 2^-13 of the largest one's power of two, toward
-// zero: at most 2^-10 of that product, and of values alike 2^-16 of the sum of
-// magnitudes.  That is a quarter of bf16's half step at worst where terms do not
-// cancel, and a factor of two in time for many rows, so bf16 results take it;
-// fp16 ones, whose step it could pass, and fp32 ones (EXACT) do not.  Experts of 4096 tokens on 4.6 GB of weights in 980 us (4.7 TB/s).
-// Gradients of 128 experts, 1536 x 2048, in 818 us (1.6 GB written; the stores
-// alone take 280, loads and products 600, loads and stores 535: the memory path
-// of a CU and its vector work are shared by all three): the codes are converted
-// to fp16, as fp32 results need every bit.
+// 8192 x 4096 x 4096 in 167 us (1.6 PFLOP/s): each 128 of the summed axis costs
+// a fused multiply-add per result beside its matrix instruction.  The sums take
+// half of the 256 x 256 tile's registers and the operands the rest but for one
+// or two results, so a matrix instruction is waited for in full by its
+// multiply-adds, and each read of P too; deeper stages, wave priorities and
+// fixed schedules changed nothing on so few registers.  The 8-bit instruction
+// adds 8 neighbouring products at a time and drops of each what is under 2^-13
+// of the largest one's power of two, toward zero: at most 2^-10 of that
+// product, and of values alike 2^-16 of the sum of magnitudes.  That is a
+// quarter of bf16's half step at worst where terms do not cancel, and a factor
+// of two in time for many rows, so bf16 results take it; fp16 ones, whose step
+// it could pass, and fp32 ones (EXACT) do not.  Experts of 4096 tokens on 4.6
+// GB of weights in 1000 us (4.6 TB/s). Gradients of 128 experts, 1536 x 2048,
+// in 850 us (1.6 GB written; taken apart, the stores alone took 280, loads and
+// products 600, loads and stores 535: the memory path of a CU and its vector
+// work are shared by all three): the codes are converted to fp16, as fp32
+// results need every bit.
 template <bool DEPTH, bool EXACT, int SUB, int NS>
 struct Tile {
   static constexpr int BM = 32 * SUB, BN = 64 * NS;
@@ -618,9 +622,14 @@ int launch_tiles(const MmArgs& m, hipStream_t s) {
 // 512 rows 25 / 32 as 128x128; 1024 rows 48 as 64x128 / 34 / 46 as 128x256;
 // 2048 rows 65 as 128x128 / 50 / 80 as 256x256; 1024 columns, 512 rows: 25 as
 // few rows, 24 as 64x128.  Experts' rows are expected to fill their last tile
-// by half; 64 experts of about 96 rows, 2048 x 2048: 112 / 97 / 90 / 96; 128 of
-// about 512 rows, unevenly, 1536 x 2048: 400 as 128x256 / 461 as 256x256, which
-// leaves more of its last tiles empty.
+// by half, and only their capacity is known here, not the rows in use: one
+// token of 8 of 128 experts, 2048 x 1536, takes 22 us on segments padded to 128
+// (1024 rows to the rule) and 14 without padding, 4, 32 and 128 tokens the same
+// on both; where the weights' bytes are the time, the table does not say it
+// (4096 tokens of 256 experts: 1690 by it, 1000 taken).  Measured choices: 64
+// experts of about 96 rows, 2048 x 2048: 112 / 97 / 90 / 96; 128 of about 512
+// rows, unevenly, 1536 x 2048: 400 as 128x256 / 461 as 256x256, which leaves
+// more of its last tiles empty.
 double rounds(double workgroups) { return std::ceil(workgroups / CUS); }
 
 double row_tiles(const MmArgs& m, bool depth, int BM) {

@@ -17,7 +17,10 @@
 // a workgroup (wider rows of the backward pass: twice).  All sums are fp32 in a
 // fixed order.  The bytes are the bound: 8192 rows of 4096, bf16 with an fp32
 // residual, take 82 us (403 MB, 4.9 TB/s, as a copy), their gradients 3.1 to
-// 3.7 TB/s; one row of 2048 takes 3 us, a launch and two trips to memory.
+// 3.7 TB/s; one row of 2048 takes 3 us, a launch and two trips to memory.  The
+// norm before a block, 8192 x 4096 bf16 in the caches: 22.9 us, 23.5 as codes;
+// its gradients with dw 66 (3.0 TB/s), as 65536 x 512 91, 16384 x 2048 71, 4096 x
+// 8192 89.
 #include "e4m3.h"
 #include "op_host.h"
 

@@ -145,17 +145,6 @@ def weight_gradient_workspace_bytes(E: int, rows: int, N: int, K: int) -> int:
     return B.moe_fp8_weight_gradient_workspace_bytes(E, rows, N, K)
 
 
-def _allocated(ws, need, x, stream):
-    """Address and size of ws, or of one allocated where it is needed."""
-    if ws is None and need and x.get_device() >= 0:
-        if stream is None:
-            ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-        else:
-            with torch.cuda.stream(stream):
-                ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-    return (None, 0) if ws is None else (A.whole("ws", ws, x.get_device(), torch.uint8), ws.numel())
-
-
 def weight_gradient(dy_t, dy_scales, x_t, x_scales, dw, offsets=None, add=False, ws=None, stream=None):
     """dw = dy^T x (or dw + dy^T x) from the transposed codes of dy [N, P(R)]
     and x [K, P(R)]: fp32 [N, K], or [E, N, K] over the rows offsets[e] ..
@@ -173,7 +162,7 @@ def weight_gradient(dy_t, dy_scales, x_t, x_scales, dw, offsets=None, add=False,
     shape = (N, K) if offsets is None else (E, N, K)
     wp = A.whole("dw", dw, dev, _F32, shape)
     op = None if offsets is None else A.whole("offsets", offsets, dev, _I32, (E + 1,))
-    sp, sn = _allocated(ws, B.moe_fp8_weight_gradient_workspace_bytes(E, rows, N, K), x_t, stream)
+    sp, sn = A.workspace(ws, B.moe_fp8_weight_gradient_workspace_bytes(E, rows, N, K), x_t, stream)
     A.launch(B.lib().moe_fp8_weight_gradient, dev, stream, dp, dsp, xp, xsp, op, E, rows, N, K, 1 if add else 0, wp, K,
              sp, sn)
 
@@ -205,6 +194,6 @@ def layer(x, router, gate_up, gate_up_scales, down, down_scales, out, ids, weigh
     if base is not None:
         _, ap, ldb, _ = A.rows("base", base, dev, T, H, A.F32_ONLY)
     ip, wp = A.whole("ids", ids, dev, _I32, (T, k)), A.whole("weights", weights, dev, _F32, (T, k))
-    sp, sn = _allocated(ws, 0 if ws is not None else B.moe_fp8_layer_workspace_bytes(T, E, k, H, I), x, stream)
+    sp, sn = A.workspace(ws, 0 if ws is not None else B.moe_fp8_layer_workspace_bytes(T, E, k, H, I), x, stream)
     A.launch(B.lib().moe_fp8_layer, dev, stream, xt, xp, ldx, rp, bp, T, E, k, H, I, gp, gs, dp, ds, ap, ldb, ot, op,
              ldo, ip, wp, sp, sn)

@@ -141,14 +141,7 @@ def backward_workspace_bytes(T: int, cols: int) -> int:
 
 
 def _workspace(ws, T, cols, x, wanted, stream):
-    if ws is None and wanted and x.get_device() >= 0:
-        need = B.moe_norm_backward_workspace_bytes(T, cols)
-        if stream is None:
-            ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-        else:
-            with torch.cuda.stream(stream):
-                ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-    return (None, 0) if ws is None else (A.whole("ws", ws, x.get_device(), torch.uint8), ws.numel())
+    return A.workspace(ws, B.moe_norm_backward_workspace_bytes(T, cols) if ws is None and wanted else 0, x, stream)
 
 
 def before_backward(dout, x, weight, dx, dweight=None, base=None, eps=1e-6, ws=None, stream=None):
